@@ -92,6 +92,8 @@ typedef enum moe_status {
 #define MOE_DEVICE_BAD_EXPERT_ID 0x1u /* an id outside [0, E): slot zeroed */
 #define MOE_DEVICE_TIMEOUT 0x2u       /* a bounded in-kernel wait gave up;
                                          outputs of that call are invalid */
+#define MOE_DEVICE_BAD_ADAPTER_ID 0x4u /* an adapter id below -1 or >= the
+                                          pool's size: taken as no adapter */
 
 /* Flags of moe_route_ex. */
 #define MOE_ROUTE_RMSNORM 0x1u /* x is a residual stream r: route
@@ -478,6 +480,101 @@ MOE_API int moe_forward_noalloc(int E, int H, int I, int top_k,
  * `stream`, copies the word to *device_status and clears it (no
  * allocation).  Errors: ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_forward_noalloc_status(void *stream, unsigned *device_status);
+
+/* ---------------------------------------------------------------------
+ * Dense feed-forward layers.  The models of the pages put two dense layers
+ * ahead of their MoE layers ("LFM2.5-24B-A2B — Packed MXFP4 Inference",
+ * table "Model and quantization": 38 MoE layers of 40).  Their weights are
+ * BF16, row-major [out][in]; activations are BF16.  These calls take no
+ * handle: shapes and pointers per call, caller-owned workspace where one is
+ * needed, the conventions above otherwise (device pointers of the current
+ * device, 16-byte aligned; only kernels are enqueued).
+ *
+ * Arithmetic: FP32 accumulation and one rounding of each output.  Unlike the
+ * expert path, which repeats the serial runner's rounding points, g, u and
+ * act(g) are not rounded on the way to h.
+ *
+ * Shapes: T >= 0 (T = 0 is accepted: forward calls enqueue nothing, the
+ * backward call zeroes the weight gradients); every other dimension a
+ * multiple of 8 in [8, 65536].
+ *
+ * Device problems (a bounded wait that gave up, a bad adapter id) are OR-ed
+ * into one status word per GPU, read by moe_dense_status. */
+
+#define MOE_ACT_SILU 0      /* g * sigmoid(g)                               */
+#define MOE_ACT_GELU 1      /* g * Phi(g), the normal distribution function */
+#define MOE_ACT_GELU_TANH 2 /* g/2 * (1 + tanh(sqrt(2/pi)(g + 0.044715 g^3))) */
+
+/* Flags of moe_gated_ffn. */
+#define MOE_FFN_RMSNORM 0x1u /* x is a residual stream r: the block runs on
+                                xn = BF16(r / sqrt(mean(r^2) + 1e-6)), which
+                                is written to x_norm (as MOE_ROUTE_RMSNORM) */
+
+/* The gated block: h = act(x Wg^T) * (x Wu^T).  x: device BF16 [T][H];
+ * w_gate, w_up: device BF16 [I][H]; h: device BF16 [T][I].  x_norm: device
+ * BF16 [T][H] with MOE_FFN_RMSNORM, else NULL.  h and x_norm must not overlap
+ * each other or an input.  Errors: ARG (shape, act, flags, overlap),
+ * NOT_DEVICE, ALIGN, UNSUPPORTED, CUDA. */
+MOE_API int moe_gated_ffn(const uint16_t *x, int T, int H, int I, const uint16_t *w_gate,
+                          const uint16_t *w_up, int act, unsigned flags, uint16_t *x_norm,
+                          uint16_t *h, void *stream);
+
+/* Bytes of device workspace of moe_gated_ffn_backward: dg and du in BF16,
+ * 4 T I bytes rounded up to 256 (256 at least).  Errors: ARG. */
+MOE_API int moe_gated_ffn_backward_workspace_bytes(int T, int H, int I, size_t *bytes);
+
+/* Gradients of the gated block.  g = x Wg^T and u = x Wu^T are computed
+ * again in FP32; with dh = dL/dh (device BF16 [T][I]),
+ *   dg = dh * u * act'(g),   du = dh * act(g)      (rounded to BF16 once, as
+ *                                                   operands of the products)
+ *   dx = dg Wg + du Wu       (device BF16 [T][H])
+ *   dw_gate = dg^T x, dw_up = du^T x    (device BF16 [I][H] each)
+ * dx may be NULL (not computed), dw_gate and dw_up may both be NULL.
+ * Workspace: device, 256-byte aligned, at least
+ * moe_gated_ffn_backward_workspace_bytes; nothing in it is kept between
+ * calls.  Calls that may run at the same time need workspaces of their own.
+ * Outputs must not overlap each other, the workspace or an input.  Results
+ * are the same bits for the same inputs.  Errors: ARG, NOT_DEVICE, ALIGN,
+ * WORKSPACE, UNSUPPORTED, CUDA. */
+MOE_API int moe_gated_ffn_backward(const uint16_t *x, int T, int H, int I,
+                                   const uint16_t *w_gate, const uint16_t *w_up, int act,
+                                   const uint16_t *dh, uint16_t *dx, uint16_t *dw_gate,
+                                   uint16_t *dw_up, void *workspace, size_t bytes, void *stream);
+
+/* Bytes of device workspace of moe_adapter_proj (0 adapters: 0 bytes; rank
+ * is then not looked at).  Errors: ARG. */
+MOE_API int moe_adapter_proj_workspace_bytes(int T, int K, int N, int n_adapters, int rank,
+                                             size_t *bytes);
+
+/* A projection shared by the tokens of many requests, with the low-rank
+ * adapter of each token's request beside it:
+ *   y[t] = W x[t] + scale[a] B[a] (A[a] x[t]) (+ residual[t]),  a = ids[t]
+ * x: device BF16 [T][K]; w: device BF16 [N][K]; residual: device BF16 [T][N]
+ * or NULL (may be y itself); lora_a: device BF16 [n_adapters][rank][K];
+ * lora_b: device BF16 [n_adapters][N][rank]; lora_scale: device FP32
+ * [n_adapters] (4-byte aligned); adapter_ids: device int32 [T] (4-byte
+ * aligned), -1 for a token without an adapter; any other id outside
+ * [0, n_adapters) is taken as -1 and sets MOE_DEVICE_BAD_ADAPTER_ID.
+ * n_adapters = 0: the plain projection; the four adapter pointers and the
+ * workspace are then NULL.  rank: a multiple of 8 in [8, 256] (adapters of a
+ * smaller rank are padded with zero rows of A and columns of B).  Tokens may
+ * name adapters in any order; tokens of one request next to each other are
+ * fastest.  An adapter with infinities or NaN reaches only the tokens that
+ * name it.  Workspace: device, 256-byte
+ * aligned; nothing in it is kept between calls; calls that may run at the
+ * same time need workspaces of their own.  y must not overlap x, w, the
+ * adapters or the workspace.  Errors: ARG, NOT_DEVICE, ALIGN, WORKSPACE,
+ * UNSUPPORTED, CUDA. */
+MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint16_t *w,
+                             const uint16_t *residual, int n_adapters, int rank,
+                             const uint16_t *lora_a, const uint16_t *lora_b,
+                             const float *lora_scale, const int32_t *adapter_ids, uint16_t *y,
+                             void *workspace, size_t bytes, void *stream);
+
+/* Device status word of the dense calls on the current device (MOE_DEVICE_*
+ * bits, accumulated since the last read): synchronises `stream`, copies the
+ * word to *device_status and clears it.  Errors: ARG, UNSUPPORTED, CUDA. */
+MOE_API int moe_dense_status(void *stream, unsigned *device_status);
 
 /* Human-readable name of a status code (static string, never NULL). */
 MOE_API const char *moe_status_string(int status);

@@ -34,6 +34,9 @@ __all__ = [
     "FWD_PHASE_GATEUP", "FWD_PHASE_DOWN", "FWD_FORCE_TCGEN05", "FWD_FORCE_MMA",
     "FUSION_NONE", "FUSION_ROUTER", "FUSION_LAYER", "moe_set_fusion",
     "DEVICE_BAD_EXPERT_ID",
+    "moe_gated_ffn", "moe_gated_ffn_backward_workspace_bytes", "moe_gated_ffn_backward",
+    "moe_adapter_proj_workspace_bytes", "moe_adapter_proj", "moe_dense_status",
+    "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FFN_RMSNORM", "DEVICE_BAD_ADAPTER_ID",
 ]
 
 ROUTE_RMSNORM = 0x1
@@ -48,6 +51,9 @@ FWD_FORCE_MMA = 0x40
 FUSION_NONE, FUSION_ROUTER, FUSION_LAYER = 0, 1, 2
 DEVICE_BAD_EXPERT_ID = 0x1
 DEVICE_TIMEOUT = 0x2
+DEVICE_BAD_ADAPTER_ID = 0x4
+ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2
+FFN_RMSNORM = 0x1
 
 
 def _p(t):
@@ -349,6 +355,146 @@ def moe_stack_set_trace(s: int, trace) -> None:
 
 def moe_stack_set_spin_limit(s: int, polls: int) -> None:
     check("moe_stack_set_spin_limit", load().moe_stack_set_spin_limit(C.c_void_p(s), int(polls)))
+
+
+# ------------------------------------------- dense feed-forward layers
+
+def _shaped(t, dtype, shape, name, what):
+    """t is a contiguous CUDA tensor of this dtype and shape, else MoEError
+    (the C calls take bare pointers and cannot check sizes)."""
+    if (t is None or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+            or not t.is_contiguous()):
+        raise MoEError(f"{name} ({what})", -1)
+
+
+def _out(t, like, shape, name, what, stream):
+    """The caller's output tensor, checked, or a new one beside `like`."""
+    if t is None:
+        t = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        if stream is not None:
+            t.record_stream(stream)
+    else:
+        _shaped(t, torch.bfloat16, shape, name, what)
+    return t
+
+
+def _workspace(ws, need, like, name, stream):
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            ws.record_stream(stream)
+    elif not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise MoEError(f"{name} (workspace)", -1)
+    return ws
+
+
+def _gated_shapes(x, w_gate, w_up, name):
+    if x is None or x.dim() != 2 or w_gate is None or w_gate.dim() != 2:
+        raise MoEError(f"{name} (shape)", -1)
+    (T, H), I = x.shape, w_gate.shape[0]
+    _shaped(x, torch.bfloat16, (T, H), name, "x")
+    _shaped(w_gate, torch.bfloat16, (I, H), name, "w_gate")
+    _shaped(w_up, torch.bfloat16, (I, H), name, "w_up")
+    return T, H, I
+
+
+def moe_gated_ffn(x, w_gate, w_up, act=ACT_SILU, h=None, flags=0, x_norm=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T): x BF16 [T, H], w_gate and w_up BF16
+    [I, H]; returns h BF16 [T, I] (a new tensor when h is None). With
+    FFN_RMSNORM x is a residual stream and x_norm [T, H] receives the
+    normalised input."""
+    T, H, I = _gated_shapes(x, w_gate, w_up, "moe_gated_ffn")
+    h = _out(h, x, (T, I), "moe_gated_ffn", "h", stream)
+    if x_norm is not None:
+        _shaped(x_norm, torch.bfloat16, (T, H), "moe_gated_ffn", "x_norm")
+    check("moe_gated_ffn", load().moe_gated_ffn(
+        _p(x), T, H, I, _p(w_gate), _p(w_up), act, flags, _p(x_norm), _p(h), _s(stream)))
+    return h
+
+
+def moe_gated_ffn_backward_workspace_bytes(T: int, H: int, I: int) -> int:
+    n = C.c_size_t()
+    check("moe_gated_ffn_backward_workspace_bytes",
+          load().moe_gated_ffn_backward_workspace_bytes(T, H, I, C.byref(n)))
+    return n.value
+
+
+def moe_gated_ffn_backward(x, w_gate, w_up, dh, act=ACT_SILU, dx=None, dw_gate=None, dw_up=None,
+                           need_dx=True, need_dw=True, workspace=None, stream=None):
+    """Gradients of moe_gated_ffn for dh = dL/dh BF16 [T, I]: returns (dx
+    [T, H], dw_gate [I, H], dw_up [I, H]), BF16; None for those not needed.
+    Outputs and workspace (uint8) that are not given are new tensors."""
+    name = "moe_gated_ffn_backward"
+    T, H, I = _gated_shapes(x, w_gate, w_up, name)
+    _shaped(dh, torch.bfloat16, (T, I), name, "dh")
+    if (not need_dx and dx is not None) or (not need_dw and (dw_gate is not None or dw_up is not None)):
+        raise MoEError(f"{name} (an output that is not needed)", -1)
+    if need_dx:
+        dx = _out(dx, x, (T, H), name, "dx", stream)
+    if need_dw:
+        dw_gate = _out(dw_gate, x, (I, H), name, "dw_gate", stream)
+        dw_up = _out(dw_up, x, (I, H), name, "dw_up", stream)
+    workspace = _workspace(workspace, moe_gated_ffn_backward_workspace_bytes(T, H, I), x, name,
+                           stream)
+    check(name, load().moe_gated_ffn_backward(
+        _p(x), T, H, I, _p(w_gate), _p(w_up), act, _p(dh), _p(dx), _p(dw_gate), _p(dw_up),
+        _p(workspace), workspace.numel(), _s(stream)))
+    return dx, dw_gate, dw_up
+
+
+def moe_adapter_proj_workspace_bytes(T: int, K: int, N: int, n_adapters: int, rank: int) -> int:
+    n = C.c_size_t()
+    check("moe_adapter_proj_workspace_bytes",
+          load().moe_adapter_proj_workspace_bytes(T, K, N, n_adapters, rank, C.byref(n)))
+    return n.value
+
+
+def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_ids=None,
+                     residual=None, y=None, workspace=None, stream=None):
+    """y[t] = w x[t] + lora_scale[a] lora_b[a] (lora_a[a] x[t]) (+ residual[t])
+    with a = adapter_ids[t] (-1: none): x BF16 [T, K], w BF16 [N, K], lora_a
+    BF16 [n, rank, K], lora_b BF16 [n, N, rank], lora_scale FP32 [n],
+    adapter_ids int32 [T]. All four adapter arguments None: the plain
+    projection. residual may be y. Returns y BF16 [T, N]."""
+    name = "moe_adapter_proj"
+    if x is None or x.dim() != 2 or w is None or w.dim() != 2:
+        raise MoEError(f"{name} (shape)", -1)
+    (T, K), N = x.shape, w.shape[0]
+    _shaped(x, torch.bfloat16, (T, K), name, "x")
+    _shaped(w, torch.bfloat16, (N, K), name, "w")
+    n = rank = 0
+    given = [t is not None for t in (lora_a, lora_b, lora_scale, adapter_ids)]
+    if any(given):
+        if not all(given) or lora_a.dim() != 3:
+            raise MoEError(f"{name} (adapters)", -1)
+        n, rank = lora_a.shape[:2]
+        if n == 0:
+            raise MoEError(f"{name} (adapters)", -1)
+        _shaped(lora_a, torch.bfloat16, (n, rank, K), name, "lora_a")
+        _shaped(lora_b, torch.bfloat16, (n, N, rank), name, "lora_b")
+        _shaped(lora_scale, torch.float32, (n,), name, "lora_scale")
+        _shaped(adapter_ids, torch.int32, (T,), name, "adapter_ids")
+    if residual is not None:
+        _shaped(residual, torch.bfloat16, (T, N), name, "residual")
+    y = _out(y, x, (T, N), name, "y", stream)
+    need = moe_adapter_proj_workspace_bytes(T, K, N, n, rank)
+    if need:
+        workspace = _workspace(workspace, need, x, name, stream)
+    else:
+        workspace = None
+    check(name, load().moe_adapter_proj(
+        _p(x), T, K, N, _p(w), _p(residual), n, rank, _p(lora_a), _p(lora_b), _p(lora_scale),
+        _p(adapter_ids), _p(y), _p(workspace), workspace.numel() if workspace is not None else 0,
+        _s(stream)))
+    return y
+
+
+def moe_dense_status(stream=None) -> int:
+    """Status bits of the dense calls on the current device since the last
+    read (synchronises `stream`), cleared."""
+    v = C.c_uint()
+    check("moe_dense_status", load().moe_dense_status(_s(stream), C.byref(v)))
+    return v.value
 
 
 # ------------------------------------------------------------- bundles

@@ -54,6 +54,14 @@ SIGNATURES = [
     ("moe_stack_get_status", _i, [_vp, _vp, C.POINTER(_u)]),
     ("moe_stack_set_spin_limit", _i, [_vp, _i]),
     ("moe_stack_set_trace", _i, [_vp, _vp, _sz]),
+    ("moe_gated_ffn", _i, [_vp, _i, _i, _i, _vp, _vp, _i, _u, _vp, _vp, _vp]),
+    ("moe_gated_ffn_backward_workspace_bytes", _i, [_i, _i, _i, C.POINTER(_sz)]),
+    ("moe_gated_ffn_backward", _i, [_vp, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz,
+                                    _vp]),
+    ("moe_adapter_proj_workspace_bytes", _i, [_i, _i, _i, _i, _i, C.POINTER(_sz)]),
+    ("moe_adapter_proj", _i, [_vp, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                              _vp]),
+    ("moe_dense_status", _i, [_vp, C.POINTER(_u)]),
 ]
 
 

@@ -15,6 +15,7 @@
 #include <new>
 
 #include "../../include/moe_mxfp4.h"
+#include "host_checks.cuh"
 #include "kernels.cuh"
 
 struct moe_ctx {
@@ -43,7 +44,9 @@ struct moe_ctx {
 
 namespace {
 
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+using moe::align_up;
+using moe::cuda_rc;
+using moe::current_device_ok;
 
 struct WsLayout {
     size_t counters, logits, h, o, x16, x16_exp;
@@ -82,35 +85,7 @@ WsLayout ws_layout(const moe_ctx *c, int maxT) {
 }
 
 int check_device_ptr(const moe_ctx *c, const void *p, size_t align) {
-    if (!p) return MOE_ERR_ARG;
-    if (((uintptr_t)p) & (align - 1)) return MOE_ERR_ALIGN;
-    cudaPointerAttributes a;
-    cudaError_t e = cudaPointerGetAttributes(&a, p);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_NOT_DEVICE;
-    }
-    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) return MOE_ERR_NOT_DEVICE;
-    if (c && a.device != c->device) return MOE_ERR_NOT_DEVICE;
-    return MOE_OK;
-}
-
-int current_device_ok(int *dev, int *sms) {
-    int d = -1;
-    if (cudaGetDevice(&d) != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-    int major = 0, n = 0;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, d) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) {
-        cudaGetLastError();
-        return MOE_ERR_CUDA;
-    }
-    if (major != 10) return MOE_ERR_UNSUPPORTED;
-    if (dev) *dev = d;
-    if (sms) *sms = n;
-    return MOE_OK;
+    return moe::check_device_memory(c ? c->device : moe::kAnyDevice, p, align);
 }
 
 int ensure_device_block(moe_ctx *c) {
@@ -143,12 +118,6 @@ int upload_table(moe_ctx *c, const moe::ExpertPtrs *host_table) {
     }
     c->loaded = true;
     return MOE_OK;
-}
-
-int cuda_rc(cudaError_t e) {
-    if (e == cudaSuccess) return MOE_OK;
-    cudaGetLastError();
-    return MOE_ERR_CUDA;
 }
 
 }  // namespace

@@ -1,0 +1,47 @@
+// dense_act.cuh — activations of the gated block and their derivatives, FP32.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "../../include/moe_mxfp4.h"
+
+namespace moe {
+
+constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2 / pi)
+constexpr float kGeluC1 = 0.044715f;
+constexpr float kSqrtHalf = 0.7071067811865476f;
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+// 1 / (1 + exp(-z)), and below the same of 2 z for the tanh form of GELU:
+// (1 + tanh z) / 2 = sigmoid(2 z), which keeps the relative precision of the
+// left tail where 1 + tanh z cancels (erfc does the same for the exact GELU).
+__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+__device__ __forceinline__ float act_value(float g, int act) {
+    if (act == MOE_ACT_SILU) return g * sigmoid_f32(g);
+    if (act == MOE_ACT_GELU) return g * (0.5f * erfcf(-g * kSqrtHalf));
+    return g * sigmoid_f32(2.0f * kGeluC0 * (g + kGeluC1 * g * g * g));
+}
+
+// act(g) and act'(g).  Where the sigmoid has reached 0 or 1 its slope is 0
+// whatever the factor beside it (which may have overflowed).
+__device__ __forceinline__ void act_value_grad(float g, int act, float &a, float &da) {
+    if (act == MOE_ACT_SILU) {
+        const float s = sigmoid_f32(g), t = s * (1.0f - s);
+        a = g * s;
+        da = s + (t > 0.f ? g * t : 0.f);
+    } else if (act == MOE_ACT_GELU) {
+        const float cdf = 0.5f * erfcf(-g * kSqrtHalf);
+        const float pdf = kInvSqrt2Pi * expf(-0.5f * g * g);
+        a = g * cdf;
+        da = cdf + (pdf > 0.f ? g * pdf : 0.f);
+    } else {
+        const float s = sigmoid_f32(2.0f * kGeluC0 * (g + kGeluC1 * g * g * g));
+        const float t = s * (1.0f - s);
+        a = g * s;
+        da = s + (t > 0.f ? g * t * (2.0f * kGeluC0 * (1.0f + 3.0f * kGeluC1 * g * g)) : 0.f);
+    }
+}
+
+}  // namespace moe
