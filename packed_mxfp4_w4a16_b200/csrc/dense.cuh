@@ -40,6 +40,12 @@ struct AdapterParams {
 cudaError_t launch_rms_norm(const uint16_t *x, int T, int H, uint16_t *xn, cudaStream_t s);
 cudaError_t launch_gated(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedParams &p, int num_sms, cudaStream_t s);
+// tcgen05 products (dense_gemm.cu)
+cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s);
+
 size_t adapter_workspace(int T, int K, int N, int n, int rank);
 cudaError_t launch_adapter_proj(const AdapterParams &p, int num_sms, cudaStream_t s);
 

@@ -1,0 +1,936 @@
+// dense_gemm.cu — the dense feed-forward products on tcgen05 (FP32
+// accumulators in TMEM, operands brought in by TMA with the 128-byte swizzle).
+//
+// One kernel body serves the five products, which differ in where their
+// operands come from and in their epilogue (M x N = sum over K):
+//   kFwd   T x I    = x Wg^T and x Wu^T side by side; h = act(g) * u
+//   kBwd   the same sums; dg and du from them and dh
+//   kDx    T x H    = dg Wg + du Wu   (K runs over the halves of [dg | du])
+//   kDw    2I x H   = [dg | du]^T x   (K = T; both operands MN-major)
+//   kProj  T x N    = x W^T + v B^T (+ residual): the adapters' inner products
+//          v and the rows of their B appended to K, one block of 64 at a time
+//   kInner v = scale (x A^T) for the adapters that a tile's tokens name
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dense.cuh"
+#include "dense_act.cuh"
+#include "gemv.cuh"
+#include "tc.cuh"
+
+namespace moe {
+
+namespace {
+
+enum Mode { kFwd, kBwd, kDx, kDw, kProj, kInner };
+
+struct GemmArgs {
+    const uint16_t *dh;        // kBwd
+    const uint16_t *residual;  // kProj, or null
+    uint16_t *out0, *out1;     // kDw: dWg, dWu; else out0
+    unsigned *status;
+    int M, N;                  // rows of the output (kDw: of one half), its columns
+    int kb, kb_half;           // K blocks of 64; kDx: of one half
+    int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
+    int n_fast;                // consecutive tiles share M (else N)
+    int act;
+    // adapters (kProj with n > 0, kInner)
+    const int32_t *ids;        // [M]
+    const float *scale;        // [n], kInner
+    const uint16_t *lora_b;    // [n][N][rank], kProj
+    uint16_t *v;               // [M][rank] BF16: written by kInner, read by kProj
+    int n, rank;
+    int per_tile, parts;       // kInner: adapters per 128 columns, or tiles per adapter
+    int groups;                // kInner: CTAs (clusters) that share a row tile's adapters
+};
+
+constexpr bool gated(int mode) { return mode == kFwd || mode == kBwd; }
+constexpr bool a_mn(int mode) { return mode == kDw; }
+constexpr bool b_mn(int mode) { return mode == kDx || mode == kDw; }
+
+// One K block of operand A: 64-row boxes of the CTA's rows from `m` on.
+template <int MODE, int CG>
+__device__ __forceinline__ void load_a(uint32_t dst, const CUtensorMap *a, const GemmArgs &g, int kb, int m,
+                                       int half, int boxes, uint32_t bar) {
+    for (int i = 0; i < boxes; ++i) {
+        if (MODE == kDx) {
+            const int h = kb >= g.kb_half;
+            tc::load3<CG>(dst + i * tc::kBox, a, (kb - h * g.kb_half) * 64, h, m + 64 * i, bar);
+        } else if (MODE == kDw) {
+            tc::load3<CG>(dst + i * tc::kBox, a, m + 64 * i, half, kb * 64, bar);
+        } else {
+            tc::load2<CG>(dst + i * tc::kBox, a, kb * 64, m + 64 * i, bar);
+        }
+    }
+}
+
+// One box (64 columns of the output, or 64 rows of Wg / Wu) of operand B.
+template <int MODE, int CG>
+__device__ __forceinline__ void load_b(uint32_t dst, const CUtensorMap *b0, const CUtensorMap *b1,
+                                       const GemmArgs &g, int kb, int n, int second, uint32_t bar) {
+    if (MODE == kDx) {
+        const int h = kb >= g.kb_half;
+        tc::load2<CG>(dst, h ? b1 : b0, n, (kb - h * g.kb_half) * 64, bar);
+    } else if (MODE == kDw) {
+        tc::load2<CG>(dst, b0, n, kb * 64, bar);
+    } else if (MODE == kInner) {  // n: the adapter, second: its first rank row
+        tc::load3<CG>(dst, b0, kb * 64, second, n, bar);
+    } else {
+        tc::load2<CG>(dst, second ? b1 : b0, kb * 64, n, bar);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_f32(uint32_t w) { return bf16_to_f32(w & 0xFFFFu); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
+// Eight neighbouring outputs of one row: columns n .. n + 7 (all inside the
+// matrix: n and N are multiples of 8).  v: the sums (gated: g), u: gated only.
+// h, dg, du, dx, dW and y are rounded here, once, from FP32; dg and du are
+// BF16 because they are operands of the next products.
+template <int MODE>
+__device__ __forceinline__ void finish8(const GemmArgs &g, int64_t row, int half, int n, const float (&v)[8],
+                                        const float (&u)[8]) {
+    float o[8];
+    if (MODE == kFwd) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = act_value(v[i], g.act) * u[i];
+        *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(o);
+    } else if (MODE == kBwd) {
+        const uint4 d = *reinterpret_cast<const uint4 *>(g.dh + row * g.N + n);
+        const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float dh = i & 1 ? hi_f32(dw[i >> 1]) : lo_f32(dw[i >> 1]);
+            float a, da;
+            act_value_grad(v[i], g.act, a, da);
+            o[i] = dh * u[i] * da;
+            p[i] = dh * a;
+        }
+        uint16_t *r = g.out0 + row * 2 * g.N + n;
+        *reinterpret_cast<uint4 *>(r) = pack8(o);
+        *reinterpret_cast<uint4 *>(r + g.N) = pack8(p);
+    } else if (MODE == kDw) {
+        *reinterpret_cast<uint4 *>((half ? g.out1 : g.out0) + row * g.N + n) = pack8(v);
+    } else {
+        if (MODE == kProj && g.residual) {
+            const uint4 d = *reinterpret_cast<const uint4 *>(g.residual + row * g.N + n);
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = v[i] + (i & 1 ? hi_f32(dw[i >> 1]) : lo_f32(dw[i >> 1]));
+            *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(o);
+        } else {
+            *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(v);
+        }
+    }
+}
+
+// ------------------------------------------------------------- adapters --
+// The tokens of one tile name some set of adapters.  A group of 128 threads
+// lists them (in order of their first token), and appends to the tile's K
+// loop blocks of 64 columns that hold several adapters side by side (64 /
+// rank of them, or 64 of one adapter's columns): the A operand holds a
+// token's v in the columns of its own adapter and zeros in the others', the B
+// operand the adapters' B rows.  So one accumulator receives every token's
+// own correction, for any mixture of adapters.
+//
+// Zeros do not hide infinities and NaN (0 * inf is NaN), and one request's
+// broken adapter must not reach another's tokens: non-finite elements of B
+// are left out of the operand, and noted; the epilogue of a tile with such a
+// note adds v * b for exactly those elements to the rows that name the
+// adapter.  Non-finite v stays in its own row.
+struct AdapterSmem {
+    int ids[256];    // of the tile's rows; -1: none
+    int list[256];   // distinct ids
+    int first[256];
+    int count;
+    int cmd;         // to the MMA thread: 1 a block is in the buffer, 2 the tile's last
+    int bad;         // a non-finite element of B was left out
+};
+
+constexpr int kGroup = 128;
+
+// Barrier of the group that tells whether `ok` holds in all of it.
+__device__ __forceinline__ bool group_all(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.red.and.pred q, 1, %2, p; selp.u32 %0, 1, 0, q; }"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(kGroup)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kGroup) : "memory"); }
+
+// ids, list and count of rows m0 .. m0 + rows - 1 (rows 128 or 256; rows past
+// M have none); tid: index in the group.
+__device__ __forceinline__ void list_adapters(AdapterSmem &s, const GemmArgs &g, int m0, int rows, int tid) {
+    for (int i = tid; i < rows; i += kGroup) {
+        int id = m0 + i < g.M ? g.ids[m0 + i] : -1;
+        if (id < -1 || id >= g.n) {
+            atomicOr(g.status, kBadAdapterStatus);
+            id = -1;
+        }
+        s.ids[i] = id;
+    }
+    group_sync();
+    for (int i = tid; i < rows; i += kGroup) {
+        const int id = s.ids[i];
+        bool first = id >= 0;
+        // runs of one request end the search at once
+        for (int j = i - 1; j >= 0 && first; --j) first = s.ids[j] != id;
+        s.first[i] = first;
+    }
+    group_sync();
+    if (tid < 32) {
+        int count = 0;
+        for (int i = tid; i < rows; i += 32) {
+            const bool f = s.first[i];
+            const unsigned m = __ballot_sync(0xffffffffu, f);
+            if (f) s.list[count + __popc(m & ((1u << tid) - 1))] = s.ids[i];
+            count += __popc(m);
+        }
+        if (tid == 0) s.count = count;
+    }
+    group_sync();
+}
+
+__device__ __forceinline__ int adapter_blocks(int count, int rank) {
+    if (rank > 64) return count * ((rank + 63) / 64);
+    const int per = 64 / rank;
+    return (count + per - 1) / per;
+}
+
+// The adapter (index in the list, or -1) and its rank column of chunk c (8
+// columns) of appended block e.
+__device__ __forceinline__ void chunk_of(int e, int c, int rank, int count, int &at, int &col) {
+    if (rank > 64) {
+        const int per = (rank + 63) / 64;
+        at = e / per;
+        col = (e % per) * 64 + c * 8;
+        if (col >= rank) at = -1;
+    } else {
+        const int per = 64 / rank, slot = c * 8 / rank;
+        at = e * per + slot;
+        col = c * 8 - slot * rank;
+        if (slot >= per || at >= count) at = -1;
+    }
+}
+
+// Bits of the non-finite elements (all exponent bits set) of two BF16.
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+    return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Appended block e into the operand tiles at `a` (this CTA's 128 rows, ids
+// from `row0` of the list's rows on, matrix rows from m on) and `b` (128
+// output columns from n on), K-major with the 128-byte swizzle: 16-byte chunk
+// c of row r lies at r * 128 + 16 (c ^ (r & 7)).  One row of each per thread.
+__device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArgs &g, int e, int m, int row0,
+                                             int n, uint8_t *a, uint8_t *b, int tid) {
+    uint4 va[8], vb[8];
+    const int id = s.ids[row0 + tid];
+    const bool in = n + tid < g.N;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        int at, col;
+        chunk_of(e, c, g.rank, s.count, at, col);
+        va[c] = vb[c] = make_uint4(0, 0, 0, 0);
+        if (at >= 0) {
+            const int ad = s.list[at];
+            if (ad == id) va[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
+            if (in)
+                vb[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)ad * g.N + n + tid) * g.rank + col));
+        }
+    }
+    bool bad = false;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const uint32_t x = non_finite(vb[c].x), y = non_finite(vb[c].y), z = non_finite(vb[c].z),
+                       w = non_finite(vb[c].w);
+        bad |= (x | y | z | w) != 0;
+        const uint32_t off = tid * 128 + 16 * (c ^ (tid & 7));
+        *reinterpret_cast<uint4 *>(a + off) = va[c];
+        *reinterpret_cast<uint4 *>(b + off) = make_uint4(vb[c].x & ~x, vb[c].y & ~y, vb[c].z & ~z, vb[c].w & ~w);
+    }
+    tc::fence_async();  // before the tensor core reads them
+    return bad;
+}
+
+// The terms that append_block left out, of row `row` with adapter id, added
+// to outputs n .. n + 7.
+__device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n, float *v) {
+    const int id = g.ids[row];
+    if (id < 0 || id >= g.n) return;
+    for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < g.rank; ++j) {
+            const uint16_t b = g.lora_b[((size_t)id * g.N + n + i) * g.rank + j];
+            if ((b & 0x7F80u) == 0x7F80u) v[i] += bf16_to_f32(g.v[row * g.rank + j]) * bf16_to_f32(b);
+        }
+}
+
+// ------------------------------------------------------- large products --
+// A pair of CTAs (cluster of 2, cta_group::2) owns 256 x 256 accumulators:
+// each CTA loads and keeps its 128 rows of A and half of B's rows, the
+// leader's MMAs read both CTAs' shared memory, and each CTA's TMEM receives
+// its 128 rows.  Gated: one CTA brings 128 rows of Wg, the other 128 of Wu,
+// so a row's g and u meet in one thread.  Persistent: pairs walk the tiles
+// with a stride of the pair count; two accumulators of 256 columns, so the
+// epilogue of one tile runs under the products of the next.
+// The projection keeps one of the six stages for appended adapter blocks, which
+// four more warps fill while the main K loop runs.
+constexpr int kBigSlots = 6;
+constexpr uint32_t kBigStage = 4 * tc::kBox;  // per CTA: A 128 x 64, B 128 x 64
+constexpr size_t kBigSmem = kBigSlots * kBigStage + 1024;
+// warp 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue, 8..11 adapters
+constexpr int big_threads(int mode) { return mode == kProj ? 384 : 256; }
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(big_threads(MODE), 1)
+big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
+           const __grid_constant__ CUtensorMap map_b1, const GemmArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    constexpr int kBigStages = MODE == kProj ? kBigSlots - 1 : kBigSlots;
+    __shared__ __align__(8) uint64_t s_full[kBigStages], s_empty[kBigStages], s_tfull[2], s_tempty[2];
+    __shared__ __align__(8) uint64_t s_xfull, s_xempty;
+    __shared__ AdapterSmem s_ad;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = tc::cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = g.mt * g.nt;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kBigStages; ++i) {
+            mbar_init(&s_full[i], 2);  // both CTAs' producers
+            mbar_init(&s_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_tfull[i], 1);
+            mbar_init(&s_tempty[i], 8);  // 4 epilogue warps of both CTAs
+        }
+        mbar_init(&s_xfull, 2);
+        mbar_init(&s_xempty, 1);
+        s_abort = 0;
+        s_ad.bad = 0;
+        mbar_fence_init();
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b0);
+        if (gated(MODE) || MODE == kDx) tc::prefetch_map(&map_b1);
+    }
+    if (warp == 2) tc::tmem_alloc<2>(&s_tmem, 512);
+    tc::fence_before();
+    tc::cluster_sync();
+    tc::fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort = &s_abort;
+    // With adapters this kernel follows kInner, which lets it start only
+    // after its own inputs were complete: just v, which kInner writes, has to
+    // be waited for, and only by the warps that read it.
+    const bool adapters = MODE == kProj && g.n > 0;
+    if (!adapters) pdl_wait();
+    pdl_launch_dependents();
+
+    // tile -> first row of the pair's tile, half (kDw), first output column
+    auto place = [&](int t, int &m, int &half, int &n) {
+        const int fast = g.n_fast ? g.nt : g.mt;
+        const int a = t % fast, b = t / fast;
+        int mt = g.n_fast ? b : a;
+        const int nt = g.n_fast ? a : b;
+        half = MODE == kDw && mt >= g.mt_half;
+        if (half) mt -= g.mt_half;
+        m = mt * 256;
+        n = nt * (gated(MODE) ? 128 : 256);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int m, half, n;
+                place(t, m, half, n);
+                m += rank * 128;
+                if (!gated(MODE)) n += rank * 128;
+#pragma unroll 1
+                for (int kb = 0; kb < g.kb; ++kb, ++it) {
+                    const int s = it % kBigStages;
+                    if (it >= kBigStages && !(ok = tc::wait(&s_empty[s], (it / kBigStages - 1) & 1, abort))) break;
+                    const uint32_t bar = tc::map_rank(smem_u32(&s_full[s]), 0), dst = smem + s * kBigStage;
+                    tc::arrive_tx_cluster(bar, kBigStage);
+                    load_a<MODE, 2>(dst, &map_a, g, kb, m, half, 2, bar);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        load_b<MODE, 2>(dst + (2 + i) * tc::kBox, &map_b0, &map_b1, g, kb, n + 64 * i, rank, bar);
+                }
+            }
+            // on the way out after a wait gave up: nothing of this CTA in
+            // flight (the leader's barriers count both CTAs' bytes)
+            if (!ok && rank == 0)
+                for (int j = it > kBigStages ? it - kBigStages : 0; j < it; ++j)
+                    mbar_wait(&s_full[j % kBigStages], (j / kBigStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t id = tc::idesc(256, 256, a_mn(MODE), b_mn(MODE));
+            int it = 0, j = 0, x = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+                const int buf = j & 1;
+                if (j >= 2 && !(ok = tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort))) break;
+                tc::fence_after();
+#pragma unroll 1
+                for (int kb = 0; kb < g.kb; ++kb, ++it) {
+                    const int s = it % kBigStages;
+                    if (!(ok = tc::wait(&s_full[s], (it / kBigStages) & 1, abort))) break;
+                    tc::fence_after();
+                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * kBigStage);
+                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * kBigStage + 2 * tc::kBox);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma<2>(tmem + buf * 256, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
+                                   db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > 0 || k > 0);
+                    tc::commit<2>(&s_empty[s]);
+                }
+                if (MODE == kProj && adapters) {
+                    for (bool last = false; ok && !last; ++x) {
+                        if (!(ok = tc::wait(&s_xfull, x & 1, abort))) break;
+                        tc::fence_after();
+                        const int cmd = *(volatile int *)&s_ad.cmd;
+                        last = cmd & 2;
+                        const uint64_t da = tc::desc<false>(smem + kBigStages * kBigStage);
+                        const uint64_t db = tc::desc<false>(smem + kBigStages * kBigStage + 2 * tc::kBox);
+                        if (cmd & 1)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma<2>(tmem + buf * 256, da + 2 * k, db + 2 * k, id, true);
+                        tc::commit<2>(&s_xempty);
+                    }
+                }
+                if (ok) tc::commit<2>(&s_tfull[buf]);
+            }
+            if (!ok && it > 0) mbar_wait(&s_empty[(it - 1) % kBigStages], ((it - 1) / kBigStages) & 1);
+            if (!ok && x > 0) mbar_wait(&s_xempty, (x - 1) & 1);
+        }
+        __syncwarp();
+    } else if (MODE == kProj && warp >= 8) {
+        if (adapters) {
+            const int tid = threadIdx.x - 256;
+            uint8_t *xa = smem_raw + (smem - smem_u32(smem_raw)) + kBigStages * kBigStage, *xb = xa + 2 * tc::kBox;
+            const uint32_t xfull = tc::map_rank(smem_u32(&s_xfull), 0);
+            const uint32_t peer_bad = tc::map_rank(smem_u32(&s_ad.bad), rank ^ 1);
+            pdl_wait();
+            int x = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int m, half, n;
+                place(t, m, half, n);
+                list_adapters(s_ad, g, m, 256, tid);
+                const int blocks = adapter_blocks(s_ad.count, g.rank);
+#pragma unroll 1
+                for (int e = 0; e < (blocks ? blocks : 1); ++e, ++x) {
+                    if (x > 0) {
+                        const bool mine = tc::wait(&s_xempty, (x - 1) & 1, abort);
+                        ok = group_all(mine);  // the whole group goes on or leaves
+                        if (!ok) break;
+                    }
+                    if (blocks) {
+                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, xa, xb, tid);
+                        if (bad) {
+                            s_ad.bad = 1;
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
+                        }
+                    }
+                    if (tid == 0) s_ad.cmd = (blocks ? 1 : 0) | (e + 1 >= blocks ? 2 : 0);
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    group_sync();
+                    if (tid == 0) tc::arrive_release_cluster(xfull);
+                }
+                group_sync();  // the list is rebuilt for the next tile
+            }
+        }
+    } else if (warp >= 4) {
+        const uint32_t base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t empty0 = tc::map_rank(smem_u32(&s_tempty[0]), 0);
+        const uint32_t empty1 = tc::map_rank(smem_u32(&s_tempty[1]), 0);
+        int j = 0;
+#pragma unroll 1
+        for (int t = pair; t < tiles; t += pairs, ++j) {
+            const int buf = j & 1;
+            const bool ok = tc::wait(&s_tfull[buf], (j >> 1) & 1, abort);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc::fence_after();
+            int m, half, n;
+            place(t, m, half, n);
+            m += rank * 128 + (warp & 3) * 32 + lane;
+            const uint32_t acc = base + buf * 256;
+            constexpr int cols = gated(MODE) ? 128 : 256;
+#pragma unroll 1
+            for (int c = 0; c < cols && n + c < g.N; c += 16) {
+                uint32_t v[16], u[16];
+                tc::tmem_ld16(acc + c, v);
+                if (gated(MODE)) tc::tmem_ld16(acc + 128 + c, u);
+                tc::tmem_wait();
+                if (m < g.M) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        if (n + c + 8 * q >= g.N) break;
+                        float fv[8], fu[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            fv[i] = __uint_as_float(v[8 * q + i]);
+                            fu[i] = gated(MODE) ? __uint_as_float(u[8 * q + i]) : 0.f;
+                        }
+                        if (MODE == kProj && adapters && *(volatile int *)&s_ad.bad)
+                            add_left_out(g, m, n + c + 8 * q, fv);
+                        finish8<MODE>(g, m, half, n + c + 8 * q, fv, fu);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::arrive_cluster(buf ? empty1 : empty0);
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
+    tc::fence_before();
+    tc::cluster_sync();  // no CTA leaves while the other may still signal or read it
+    if (warp == 2) {
+        tc::fence_after();
+        tc::tmem_free<2>(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------- small products --
+// One CTA (cta_group::1) owns 128 x 128 accumulators (gated: 64 columns of g
+// and the same 64 of u; kInner: the A rows of the adapters that fit in 128
+// columns, one tile after the other while the row tile names more of them).
+// Where the tiles are too few for the SMs, a cluster of S CTAs splits K (and
+// the appended adapter blocks): every CTA leaves its partial sums in shared
+// memory, and each then finishes its share of the rows, adding the S parts in
+// rank order through distributed shared memory (the same bits every time, and
+// no workspace or counter that two calls could share).
+constexpr uint32_t kSmallStage = 4 * tc::kBox;
+constexpr int kSmallMaxStages = 6;
+constexpr int kSmallThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 adapters; all finish rows
+constexpr int kPartPitch = 132;     // floats per row of partial sums (528 bytes: spreads banks)
+static_assert(128 * kPartPitch * 4 <= 3 * kSmallStage, "the parts fit in three stages");
+
+template <int MODE>
+__global__ void __launch_bounds__(kSmallThreads, 2)
+small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
+             const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[kSmallMaxStages], s_empty[kSmallMaxStages], s_done, s_xfull, s_xempty;
+    __shared__ AdapterSmem s_ad;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *const base = smem_raw + (smem - smem_u32(smem_raw));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % splits, t = blockIdx.x / splits;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 1);
+        }
+        mbar_init(&s_done, 1);
+        mbar_init(&s_xfull, 1);
+        mbar_init(&s_xempty, 1);
+        s_abort = 0;
+        s_ad.bad = 0;
+        mbar_fence_init();
+        tc::prefetch_map(&map_a);
+        tc::prefetch_map(&map_b0);
+        if (gated(MODE) || MODE == kDx) tc::prefetch_map(&map_b1);
+    }
+    if (warp == 2) tc::tmem_alloc<1>(&s_tmem, 128);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = s_tmem;
+    volatile int *abort = &s_abort;
+    // as in big_kernel, only v has to be waited for after kInner
+    const bool adapters = MODE == kProj && g.n > 0;
+    if (!adapters) pdl_wait();
+    pdl_launch_dependents();
+
+    int mt, nt = 0;
+    if (MODE == kInner) {
+        mt = t / g.groups;
+    } else {
+        const int fast = g.n_fast ? g.nt : g.mt;
+        mt = g.n_fast ? t / fast : t % fast;
+        nt = g.n_fast ? t % fast : t / fast;
+    }
+    const int half = MODE == kDw && mt >= g.mt_half;
+    if (half) mt -= g.mt_half;
+    const int m0 = mt * 128, n0 = nt * (gated(MODE) ? 64 : 128);
+    const int kb0 = (int)((int64_t)g.kb * rank / splits), kb1 = (int)((int64_t)g.kb * (rank + 1) / splits);
+    const int rows = min(128, g.M - m0);
+    // kInner: this row tile's adapters, `per_tile` of them (or a part of one) at a time
+    const int lines = MODE == kInner ? min(g.rank, 128) : 1;
+    int w0 = 0, w1 = 1, wstep = 1;
+    if (MODE == kInner) {
+        if (warp >= 4) list_adapters(s_ad, g, m0, 128, threadIdx.x - 128);
+        __syncthreads();
+        w0 = t % g.groups;
+        w1 = g.parts > 1 ? s_ad.count * g.parts : (s_ad.count + g.per_tile - 1) / g.per_tile;
+        wstep = g.groups;
+    }
+    int it = 0, round = 0;
+#pragma unroll 1
+    for (int w = w0; w < w1; w += wstep, ++round) {
+        const int part = MODE == kInner ? w % g.parts : 0;
+        const int a0 = MODE == kInner ? w / g.parts * g.per_tile : 0;
+        const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
+        if (warp == 0) {
+            if (lane == 0) {
+                const int boxes = rows > 64 ? 2 : 1;  // rows beyond are garbage that stays in its rows
+                const uint32_t bytes = boxes * tc::kBox + (MODE == kInner ? slots * lines * 128 : 2 * tc::kBox);
+                bool ok = !*abort;
+                const int it0 = it;
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                    const int s = it % stages;
+                    if (it >= stages && !(ok = tc::wait(&s_empty[s], (it / stages - 1) & 1, abort))) break;
+                    const uint32_t bar = smem_u32(&s_full[s]), dst = smem + s * kSmallStage;
+                    mbar_arrive_expect_tx(&s_full[s], bytes);
+                    if (MODE == kInner) {
+                        for (int i = 0; i < slots; ++i)
+                            load_b<MODE, 1>(dst + 2 * tc::kBox + i * lines * 128, &map_b0, &map_b1, g, kb,
+                                            s_ad.list[a0 + i], part * 128, bar);
+                    } else {
+                        load_b<MODE, 1>(dst + 2 * tc::kBox, &map_b0, &map_b1, g, kb, n0, 0, bar);
+                        load_b<MODE, 1>(dst + 3 * tc::kBox, &map_b0, &map_b1, g, kb, gated(MODE) ? n0 : n0 + 64, 1,
+                                        bar);
+                    }
+                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, boxes, bar);
+                }
+                if (!ok)
+                    for (int j = it > it0 + stages ? it - stages : it0; j < it; ++j)
+                        mbar_wait(&s_full[j % stages], (j / stages) & 1);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (lane == 0) {
+                constexpr uint32_t id = tc::idesc(128, 128, a_mn(MODE), b_mn(MODE));
+                bool ok = !*abort;
+                int x = 0;
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
+                    const int s = it % stages;
+                    if (!(ok = tc::wait(&s_full[s], (it / stages) & 1, abort))) break;
+                    tc::fence_after();
+                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * kSmallStage);
+                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * kSmallStage + 2 * tc::kBox);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc::mma<1>(tmem, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
+                                   db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > kb0 || k > 0);
+                    tc::commit<1>(&s_empty[s]);
+                }
+                if (MODE == kProj && adapters) {
+                    for (bool last = false; ok && !last; ++x) {
+                        if (!(ok = tc::wait(&s_xfull, x & 1, abort))) break;
+                        tc::fence_after();
+                        const int cmd = *(volatile int *)&s_ad.cmd;
+                        last = cmd & 2;
+                        const uint64_t da = tc::desc<false>(smem + stages * kSmallStage);
+                        const uint64_t db = tc::desc<false>(smem + stages * kSmallStage + 2 * tc::kBox);
+                        if (cmd & 1)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, id, true);
+                        tc::commit<1>(&s_xempty);
+                    }
+                }
+                tc::commit<1>(&s_done);
+                if (!ok) mbar_wait(&s_done, round & 1);
+            }
+            __syncwarp();
+        } else if (MODE == kProj && warp >= 4 && adapters) {
+            const int tid = threadIdx.x - 128;
+            pdl_wait();
+            list_adapters(s_ad, g, m0, 128, tid);
+            const int blocks = adapter_blocks(s_ad.count, g.rank);
+            const int e0 = blocks * rank / splits, e1 = blocks * (rank + 1) / splits;
+            uint8_t *xa = base + stages * kSmallStage;
+            int x = 0;
+#pragma unroll 1
+            for (int e = e0; e < max(e1, e0 + 1); ++e, ++x) {
+                if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort))) break;
+                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, xa, xa + 2 * tc::kBox, tid)) s_ad.bad = 1;
+                if (tid == 0) s_ad.cmd = (e < e1 ? 1 : 0) | (e + 1 >= e1 ? 2 : 0);
+                group_sync();
+                if (tid == 0) mbar_arrive(&s_xfull);
+            }
+        }
+        // every warp: the sums are complete (so all copies have been used too)
+        const bool ok = tc::wait(&s_done, round & 1, abort);
+        if (__syncthreads_and(ok)) {
+            tc::fence_after();
+            // TMEM -> shared memory: warp w takes lanes 32 (w % 4) .., half of the columns
+            float *parts = reinterpret_cast<float *>(base);
+            const int r = (warp & 3) * 32 + lane;
+            const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+            for (int c = (warp >> 2) * 64; c < (warp >> 2) * 64 + 64; c += 16) {
+                uint32_t v[16];
+                tc::tmem_ld16(acc + c, v);
+                tc::tmem_wait();
+#pragma unroll
+                for (int q = 0; q < 16; q += 4)
+                    *reinterpret_cast<uint4 *>(parts + r * kPartPitch + c + q) =
+                        make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+            }
+        }
+        tc::fence_before();
+        if (splits > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+        if (!s_abort) {
+            constexpr int per_row = gated(MODE) ? 8 : 16;  // groups of 8 outputs
+            const int share = (rows + splits - 1) / splits;
+            const int r0 = rank * share, r1 = min(rows, r0 + share);
+            int bad = 0;
+            if (MODE == kProj && adapters)
+                for (int q = 0; q < splits; ++q)
+                    bad |= tc::ld_cluster(splits > 1 ? tc::map_rank(smem_u32(&s_ad.bad), q) : smem_u32(&s_ad.bad));
+            for (int i = threadIdx.x; i < (r1 - r0) * per_row; i += kSmallThreads) {
+                const int r = r0 + i / per_row, c = (i % per_row) * 8;
+                int id = 0;
+                if (MODE == kInner) {
+                    const int slot = c / lines;
+                    if (slot >= slots || part * 128 + c - slot * lines >= g.rank) continue;
+                    id = s_ad.ids[r];
+                    if (s_ad.list[a0 + slot] != id) continue;
+                } else if (n0 + c >= g.N) {
+                    continue;
+                }
+                float v[8] = {}, u[8] = {};
+                const uint32_t at = smem + (uint32_t)(r * kPartPitch + c) * 4;
+                for (int q = 0; q < splits; ++q) {
+                    const uint32_t from = splits > 1 ? tc::map_rank(at, q) : at;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 a = tc::ld_cluster16(from + 16 * j);
+                        v[4 * j] += a.x, v[4 * j + 1] += a.y, v[4 * j + 2] += a.z, v[4 * j + 3] += a.w;
+                        if (gated(MODE)) {
+                            const float4 b = tc::ld_cluster16(from + 256 + 16 * j);
+                            u[4 * j] += b.x, u[4 * j + 1] += b.y, u[4 * j + 2] += b.z, u[4 * j + 3] += b.w;
+                        }
+                    }
+                }
+                if (MODE == kInner) {
+                    const float sc = g.scale[id];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] *= sc;
+                    // rounded to BF16: an operand of the projection's appended blocks
+                    *reinterpret_cast<uint4 *>(g.v + (size_t)(m0 + r) * g.rank + part * 128 + c % lines) = pack8(v);
+                    continue;
+                }
+                if (MODE == kProj && bad) add_left_out(g, (int64_t)m0 + r, n0 + c, v);
+                finish8<MODE>(g, (int64_t)m0 + r, half, n0 + c, v, u);
+            }
+        }
+        if (MODE == kInner) tc::fence_async();  // the parts' space becomes stages again
+        // no CTA goes on (or leaves) while another reads its parts
+        if (splits > 1)
+            tc::cluster_sync();
+        else
+            __syncthreads();
+    }
+    if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
+    if (warp == 2) {
+        tc::fence_after();
+        tc::tmem_free<1>(tmem, 128);
+    }
+}
+
+// ------------------------------------------------------------------- host --
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                           cudaStream_t s, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+struct Maps {
+    CUtensorMap a, b0, b1;
+};
+
+constexpr int kMaxSplits = 8;  // portable cluster size
+
+template <int MODE>
+cudaError_t launch_small(const Maps &m, const GemmArgs &g, int64_t tiles, int num_sms, cudaStream_t s) {
+    static PerDeviceOnce once;
+    const cudaError_t e = per_device_once(once, [] {
+        return cudaFuncSetAttribute(small_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(kSmallMaxStages * kSmallStage + 1024));
+    });
+    if (e != cudaSuccess) return e;
+    int splits = 1;
+    while (splits < kMaxSplits && tiles * splits < num_sms && 2 * splits <= g.kb / 2) splits *= 2;
+    // one slot is for appended adapter blocks
+    const int slots = tiles * splits > num_sms ? 3 : kSmallMaxStages;
+    const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);
+    return launch_cluster(small_kernel<MODE>, (unsigned)(tiles * splits), kSmallThreads,
+                          (size_t)slots * kSmallStage + 1024, splits > 1 ? splits : 0, s, m.a, m.b0, m.b1, g,
+                          stages, splits);
+}
+
+template <int MODE>
+cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
+    static PerDeviceOnce once;
+    const cudaError_t e = per_device_once(once, [] {
+        return cudaFuncSetAttribute(big_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
+    });
+    if (e != cudaSuccess) return e;
+    const int halves = MODE == kDw ? 2 : 1;
+    const int bn = gated(MODE) ? 128 : 256;
+    // Pairs of CTAs when their 256-row tiles fill the GPU; else single CTAs,
+    // K split over a cluster until the GPU is filled.
+    const int64_t big_tiles = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, bn);
+    if (g.M > 128 && big_tiles >= num_sms / 2) {
+        g.mt_half = ceil_div(g.M, 256);
+        g.mt = g.mt_half * halves;
+        g.nt = ceil_div(g.N, bn);
+        g.n_fast = g.nt < g.mt;
+        const int pairs = (int)(big_tiles < num_sms / 2 ? big_tiles : num_sms / 2);
+        return launch_cluster(big_kernel<MODE>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
+    }
+    g.mt_half = ceil_div(g.M, 128);
+    g.mt = g.mt_half * halves;
+    g.nt = ceil_div(g.N, bn / 2);
+    g.n_fast = g.nt < g.mt;
+    return launch_small<MODE>(m, g, (int64_t)g.mt * g.nt, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+    Maps m;
+    cudaError_t e = tc::map_matrix(&m.a, p.x, p.T, p.H);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
+    if (e != cudaSuccess) return e;
+    GemmArgs g = {};
+    g.status = p.status;
+    g.M = p.T;
+    g.N = p.I;
+    g.kb = ceil_div(p.H, 64);
+    g.act = p.act;
+    if (p.h) {
+        g.out0 = p.h;
+        return launch_gemm<kFwd>(m, g, num_sms, s);
+    }
+    g.dh = p.dh;
+    g.out0 = p.dgu;
+    return launch_gemm<kBwd>(m, g, num_sms, s);
+}
+
+cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+    Maps m;
+    cudaError_t e = tc::map_halves(&m.a, p.dgu, p.T, p.I);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
+    if (e != cudaSuccess) return e;
+    GemmArgs g = {};
+    g.status = p.status;
+    g.M = p.T;
+    g.N = p.H;
+    g.kb_half = ceil_div(p.I, 64);
+    g.kb = 2 * g.kb_half;
+    g.out0 = p.dx;
+    return launch_gemm<kDx>(m, g, num_sms, s);
+}
+
+cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+    Maps m;
+    cudaError_t e = tc::map_halves(&m.a, p.dgu, p.T, p.I);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.x, p.T, p.H);
+    if (e != cudaSuccess) return e;
+    m.b1 = m.b0;
+    GemmArgs g = {};
+    g.status = p.status;
+    g.M = p.I;
+    g.N = p.H;
+    g.kb = ceil_div(p.T, 64);
+    g.out0 = p.dwg;
+    g.out1 = p.dwu;
+    return launch_gemm<kDw>(m, g, num_sms, s);
+}
+
+cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) {
+    Maps m;
+    cudaError_t e = tc::map_matrix(&m.a, p.x, p.T, p.K);
+    if (e != cudaSuccess) return e;
+    GemmArgs g = {};
+    g.status = p.status;
+    g.M = p.T;
+    g.kb = ceil_div(p.K, 64);
+    g.ids = p.ids;
+    g.scale = p.scale;
+    g.lora_b = p.b;
+    g.v = reinterpret_cast<uint16_t *>(p.v);
+    g.n = p.n;
+    g.rank = p.rank;
+    if (p.n > 0) {
+        const int lines = p.rank < 128 ? p.rank : 128;
+        if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
+        m.b1 = m.b0;
+        g.per_tile = 128 / lines;
+        g.parts = ceil_div(p.rank, 128);
+        g.mt = ceil_div(p.T, 128);
+        // as many clusters per row tile as its adapters could use, while they fit the GPU
+        const int most = p.n < 128 ? p.n : 128;
+        const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
+        g.groups = num_sms / g.mt;
+        if (g.groups < 1) g.groups = 1;
+        if (g.groups > tiles) g.groups = tiles;
+        e = launch_small<kInner>(m, g, (int64_t)g.mt * g.groups, num_sms, s);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = tc::map_matrix(&m.b0, p.w, p.N, p.K)) != cudaSuccess) return e;
+    m.b1 = m.b0;
+    g.N = p.N;
+    g.residual = p.residual;
+    g.out0 = p.y;
+    return launch_gemm<kProj>(m, g, num_sms, s);
+}
+
+}  // namespace moe

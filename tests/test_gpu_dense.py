@@ -78,6 +78,20 @@ def test_gated_backward_against_differences(act):
             assert abs((up - dn) / (2 * eps) - float(grad.view(-1)[flat])) < 1e-6
 
 
+@pytest.mark.parametrize("T,H,I,act", [(2600, 1800, 1304, "silu"), (2561, 2048, 1536, "gelu_tanh"),
+                                       (4000, 1288, 72, "gelu")])
+def test_gated_many_tokens(T, H, I, act):
+    """Enough 256-row tiles for the CTA pairs, ragged and full, several per pair."""
+    x, wg, wu = gated_inputs(T, H, I, seed=T)
+    h = moe.moe_gated_ffn(x, wg, wu, ACTS[act])
+    assert_within(h, *gated64(x, wg, wu, act), f"h {T}x{H}x{I} {act}")
+    dh = normal((T, I), 0.1, T + 50)
+    got = moe.moe_gated_ffn_backward(x, wg, wu, dh, ACTS[act])
+    want, bound = gated_backward64(x, wg, wu, dh, act)
+    for g, w, b, what in zip(got, want, bound, ("dx", "dw_gate", "dw_up")):
+        assert_within(g, w, b, f"{what} {T}x{H}x{I} {act}")
+
+
 def test_gated_backward_parts_alone():
     x, wg, wu = gated_inputs(70, 136, 200, seed=1)
     dh = normal((70, 200), 0.1, 2)
@@ -144,6 +158,14 @@ PROJ = [(8, 8, 8, 1), (136, 72, 24, 3), (384, 512, 16, 20), (1000, 520, 64, 7), 
 @pytest.mark.parametrize("T", TOKENS)
 def test_adapter_proj(T, K, N, rank, n):
     check_adapter(adapter_inputs(T, K, N, rank, n, runs=T % 2 == 1, seed=T), f"y {T} {K} {N} {rank} {n}")
+
+
+@pytest.mark.parametrize("T,K,N,rank,n,runs", [(2600, 520, 1800, 16, 9, True), (2561, 264, 2048, 40, 30, False),
+                                               (5000, 136, 1032, 128, 3, True)])
+def test_adapter_proj_many_tokens(T, K, N, rank, n, runs):
+    d = adapter_inputs(T, K, N, rank, n, runs, seed=T)
+    check_adapter(d, f"y {T} {K} {N} {rank} {n}")
+    check_adapter({"x": d["x"], "w": d["w"], "residual": d["residual"]}, "plain")
 
 
 @pytest.mark.parametrize("T", [1, 5, 8, 40, 200])
