@@ -362,9 +362,20 @@ def moe_stack_set_spin_limit(s: int, polls: int) -> None:
 def _shaped(t, dtype, shape, name, what):
     """t is a contiguous CUDA tensor of this dtype and shape, else MoEError
     (the C calls take bare pointers and cannot check sizes)."""
-    if (t is None or not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-            or not t.is_contiguous()):
+    if t is None or not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise MoEError(f"{name} ({what})", -1)
+
+
+def _raw_stream(stream, like):
+    """cudaStream_t of `stream`, or of the current stream of the device of
+    `like` (the C calls refuse memory of any but the current device)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _out(t, like, shape, name, what, stream):
@@ -408,7 +419,7 @@ def moe_gated_ffn(x, w_gate, w_up, act=ACT_SILU, h=None, flags=0, x_norm=None, s
     if x_norm is not None:
         _shaped(x_norm, torch.bfloat16, (T, H), "moe_gated_ffn", "x_norm")
     check("moe_gated_ffn", load().moe_gated_ffn(
-        _p(x), T, H, I, _p(w_gate), _p(w_up), act, flags, _p(x_norm), _p(h), _s(stream)))
+        _ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), act, flags, _ptr(x_norm), _ptr(h), _raw_stream(stream, x)))
     return h
 
 
@@ -437,8 +448,8 @@ def moe_gated_ffn_backward(x, w_gate, w_up, dh, act=ACT_SILU, dx=None, dw_gate=N
     workspace = _workspace(workspace, moe_gated_ffn_backward_workspace_bytes(T, H, I), x, name,
                            stream)
     check(name, load().moe_gated_ffn_backward(
-        _p(x), T, H, I, _p(w_gate), _p(w_up), act, _p(dh), _p(dx), _p(dw_gate), _p(dw_up),
-        _p(workspace), workspace.numel(), _s(stream)))
+        _ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), act, _ptr(dh), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
+        _ptr(workspace), workspace.numel(), _raw_stream(stream, x)))
     return dx, dw_gate, dw_up
 
 
@@ -483,9 +494,9 @@ def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_id
     else:
         workspace = None
     check(name, load().moe_adapter_proj(
-        _p(x), T, K, N, _p(w), _p(residual), n, rank, _p(lora_a), _p(lora_b), _p(lora_scale),
-        _p(adapter_ids), _p(y), _p(workspace), workspace.numel() if workspace is not None else 0,
-        _s(stream)))
+        _ptr(x), T, K, N, _ptr(w), _ptr(residual), n, rank, _ptr(lora_a), _ptr(lora_b), _ptr(lora_scale),
+        _ptr(adapter_ids), _ptr(y), _ptr(workspace), workspace.numel() if workspace is not None else 0,
+        _raw_stream(stream, x)))
     return y
 
 

@@ -13,27 +13,32 @@ constexpr float kGeluC1 = 0.044715f;
 constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// 1 / (1 + exp(-z)), and below the same of 2 z for the tanh form of GELU:
-// (1 + tanh z) / 2 = sigmoid(2 z), which keeps the relative precision of the
-// left tail where 1 + tanh z cancels (erfc does the same for the exact GELU).
-__device__ __forceinline__ float sigmoid_f32(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 1 / (1 + exp(-z)), by the hardware's 2^x and reciprocal (a few 2^-23
+// relative for |z| of order 1, |z| 2^-23 in the left tail: far below the
+// 2^-8 of the BF16 results).  Below the same of 2 z serves the tanh form of
+// GELU: (1 + tanh z) / 2 = sigmoid(2 z), which keeps the relative precision
+// of the left tail where 1 + tanh z cancels (erfc does the same for the
+// exact GELU).
+__device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
-__device__ __forceinline__ float act_value(float g, int act) {
-    if (act == MOE_ACT_SILU) return g * sigmoid_f32(g);
-    if (act == MOE_ACT_GELU) return g * (0.5f * erfcf(-g * kSqrtHalf));
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    if (ACT == MOE_ACT_SILU) return g * sigmoid_f32(g);
+    if (ACT == MOE_ACT_GELU) return g * (0.5f * erfcf(-g * kSqrtHalf));
     return g * sigmoid_f32(2.0f * kGeluC0 * (g + kGeluC1 * g * g * g));
 }
 
 // act(g) and act'(g).  Where the sigmoid has reached 0 or 1 its slope is 0
 // whatever the factor beside it (which may have overflowed).
-__device__ __forceinline__ void act_value_grad(float g, int act, float &a, float &da) {
-    if (act == MOE_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ void act_value_grad(float g, float &a, float &da) {
+    if (ACT == MOE_ACT_SILU) {
         const float s = sigmoid_f32(g), t = s * (1.0f - s);
         a = g * s;
         da = s + (t > 0.f ? g * t : 0.f);
-    } else if (act == MOE_ACT_GELU) {
+    } else if (ACT == MOE_ACT_GELU) {
         const float cdf = 0.5f * erfcf(-g * kSqrtHalf);
-        const float pdf = kInvSqrt2Pi * expf(-0.5f * g * g);
+        const float pdf = kInvSqrt2Pi * __expf(-0.5f * g * g);
         a = g * cdf;
         da = cdf + (pdf > 0.f ? g * pdf : 0.f);
     } else {

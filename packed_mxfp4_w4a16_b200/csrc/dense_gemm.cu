@@ -33,7 +33,6 @@ struct GemmArgs {
     int kb, kb_half;           // K blocks of 64; kDx: of one half
     int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
     int n_fast;                // consecutive tiles share M (else N)
-    int act;
     // adapters (kProj with n > 0, kInner)
     const int32_t *ids;        // [M]
     const float *scale;        // [n], kInner
@@ -96,13 +95,13 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // matrix: n and N are multiples of 8).  v: the sums (gated: g), u: gated only.
 // h, dg, du, dx, dW and y are rounded here, once, from FP32; dg and du are
 // BF16 because they are operands of the next products.
-template <int MODE>
+template <int MODE, int ACT>
 __device__ __forceinline__ void finish8(const GemmArgs &g, int64_t row, int half, int n, const float (&v)[8],
                                         const float (&u)[8]) {
     float o[8];
     if (MODE == kFwd) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = act_value(v[i], g.act) * u[i];
+        for (int i = 0; i < 8; ++i) o[i] = act_value<ACT>(v[i]) * u[i];
         *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(o);
     } else if (MODE == kBwd) {
         const uint4 d = *reinterpret_cast<const uint4 *>(g.dh + row * g.N + n);
@@ -112,7 +111,7 @@ __device__ __forceinline__ void finish8(const GemmArgs &g, int64_t row, int half
         for (int i = 0; i < 8; ++i) {
             const float dh = i & 1 ? hi_f32(dw[i >> 1]) : lo_f32(dw[i >> 1]);
             float a, da;
-            act_value_grad(v[i], g.act, a, da);
+            act_value_grad<ACT>(v[i], a, da);
             o[i] = dh * u[i] * da;
             p[i] = dh * a;
         }
@@ -289,16 +288,20 @@ __device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n,
 // The projection keeps one of the six stages for appended adapter blocks, which
 // four more warps fill while the main K loop runs.
 constexpr int kBigSlots = 6;
+constexpr int kStrip = 8;
 constexpr uint32_t kBigStage = 4 * tc::kBox;  // per CTA: A 128 x 64, B 128 x 64
 constexpr size_t kBigSmem = kBigSlots * kBigStage + 1024;
-// warp 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue, 8..11 adapters
-constexpr int big_threads(int mode) { return mode == kProj ? 384 : 256; }
+// warp 0 TMA, 1 MMA, 2 TMEM, 4..7 epilogue; 8..11 adapters (kProj) or four
+// more epilogue warps (gated: the activations of a 128-row tile took four
+// warps longer than the products of a K of 2048)
+constexpr int big_threads(int mode) { return mode == kProj || gated(mode) ? 384 : 256; }
 
-template <int MODE>
+template <int MODE, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(big_threads(MODE), 1)
 big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
            const __grid_constant__ CUtensorMap map_b1, const GemmArgs g) {
     extern __shared__ uint8_t smem_raw[];
+    constexpr int kEpi = gated(MODE) ? 8 : 4;
     constexpr int kBigStages = MODE == kProj ? kBigSlots - 1 : kBigSlots;
     __shared__ __align__(8) uint64_t s_full[kBigStages], s_empty[kBigStages], s_tfull[2], s_tempty[2];
     __shared__ __align__(8) uint64_t s_xfull, s_xempty;
@@ -318,7 +321,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_tfull[i], 1);
-            mbar_init(&s_tempty[i], 8);  // 4 epilogue warps of both CTAs
+            mbar_init(&s_tempty[i], 2 * kEpi);  // the epilogue warps of both CTAs
         }
         mbar_init(&s_xfull, 2);
         mbar_init(&s_xempty, 1);
@@ -344,8 +347,12 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 
     // tile -> first row of the pair's tile, half (kDw), first output column
     auto place = [&](int t, int &m, int &half, int &n) {
-        const int fast = g.n_fast ? g.nt : g.mt;
-        const int a = t % fast, b = t / fast;
+        // strips of up to 8 tiles along the shorter dimension: the tiles of one
+        // moment form a block that shares operands in L2
+        const int fast = g.n_fast ? g.nt : g.mt, slow = g.n_fast ? g.mt : g.nt;
+        const int strip = t / (kStrip * slow), at = t - strip * kStrip * slow;
+        const int width = min(kStrip, fast - strip * kStrip);
+        const int a = strip * kStrip + at % width, b = at / width;
         int mt = g.n_fast ? b : a;
         const int nt = g.n_fast ? a : b;
         half = MODE == kDw && mt >= g.mt_half;
@@ -479,9 +486,11 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             place(t, m, half, n);
             m += rank * 128 + (warp & 3) * 32 + lane;
             const uint32_t acc = base + buf * 256;
-            constexpr int cols = gated(MODE) ? 128 : 256;
+            // gated: two warps share the rows, each finishes half of the columns
+            const int c0 = gated(MODE) && warp >= 8 ? 64 : 0;
+            const int c1 = gated(MODE) ? c0 + 64 : 256;
 #pragma unroll 1
-            for (int c = 0; c < cols && n + c < g.N; c += 16) {
+            for (int c = c0; c < c1 && n + c < g.N; c += 16) {
                 uint32_t v[16], u[16];
                 tc::tmem_ld16(acc + c, v);
                 if (gated(MODE)) tc::tmem_ld16(acc + 128 + c, u);
@@ -498,7 +507,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         }
                         if (MODE == kProj && adapters && *(volatile int *)&s_ad.bad)
                             add_left_out(g, m, n + c + 8 * q, fv);
-                        finish8<MODE>(g, m, half, n + c + 8 * q, fv, fu);
+                        finish8<MODE, ACT>(g, m, half, n + c + 8 * q, fv, fu);
                     }
                 }
             }
@@ -532,7 +541,7 @@ constexpr int kSmallThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 adapters;
 constexpr int kPartPitch = 132;     // floats per row of partial sums (528 bytes: spreads banks)
 static_assert(128 * kPartPitch * 4 <= 3 * kSmallStage, "the parts fit in three stages");
 
-template <int MODE>
+template <int MODE, int ACT>
 __global__ void __launch_bounds__(kSmallThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
              const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits) {
@@ -748,7 +757,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     continue;
                 }
                 if (MODE == kProj && bad) add_left_out(g, (int64_t)m0 + r, n0 + c, v);
-                finish8<MODE>(g, (int64_t)m0 + r, half, n0 + c, v, u);
+                finish8<MODE, ACT>(g, (int64_t)m0 + r, half, n0 + c, v, u);
             }
         }
         if (MODE == kInner) tc::fence_async();  // the parts' space becomes stages again
@@ -795,11 +804,11 @@ struct Maps {
 
 constexpr int kMaxSplits = 8;  // portable cluster size
 
-template <int MODE>
+template <int MODE, int ACT>
 cudaError_t launch_small(const Maps &m, const GemmArgs &g, int64_t tiles, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
-        return cudaFuncSetAttribute(small_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(small_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(kSmallMaxStages * kSmallStage + 1024));
     });
     if (e != cudaSuccess) return e;
@@ -808,16 +817,16 @@ cudaError_t launch_small(const Maps &m, const GemmArgs &g, int64_t tiles, int nu
     // one slot is for appended adapter blocks
     const int slots = tiles * splits > num_sms ? 3 : kSmallMaxStages;
     const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);
-    return launch_cluster(small_kernel<MODE>, (unsigned)(tiles * splits), kSmallThreads,
+    return launch_cluster(small_kernel<MODE, ACT>, (unsigned)(tiles * splits), kSmallThreads,
                           (size_t)slots * kSmallStage + 1024, splits > 1 ? splits : 0, s, m.a, m.b0, m.b1, g,
                           stages, splits);
 }
 
-template <int MODE>
+template <int MODE, int ACT>
 cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
-        return cudaFuncSetAttribute(big_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
+        return cudaFuncSetAttribute(big_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
     });
     if (e != cudaSuccess) return e;
     const int halves = MODE == kDw ? 2 : 1;
@@ -831,13 +840,20 @@ cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) 
         g.nt = ceil_div(g.N, bn);
         g.n_fast = g.nt < g.mt;
         const int pairs = (int)(big_tiles < num_sms / 2 ? big_tiles : num_sms / 2);
-        return launch_cluster(big_kernel<MODE>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
+        return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
     }
     g.mt_half = ceil_div(g.M, 128);
     g.mt = g.mt_half * halves;
     g.nt = ceil_div(g.N, bn / 2);
     g.n_fast = g.nt < g.mt;
-    return launch_small<MODE>(m, g, (int64_t)g.mt * g.nt, num_sms, s);
+    return launch_small<MODE, ACT>(m, g, (int64_t)g.mt * g.nt, num_sms, s);
+}
+
+template <int MODE>
+cudaError_t launch_act(int act, const Maps &m, const GemmArgs &g, int num_sms, cudaStream_t s) {
+    if (act == MOE_ACT_SILU) return launch_gemm<MODE, MOE_ACT_SILU>(m, g, num_sms, s);
+    if (act == MOE_ACT_GELU) return launch_gemm<MODE, MOE_ACT_GELU>(m, g, num_sms, s);
+    return launch_gemm<MODE, MOE_ACT_GELU_TANH>(m, g, num_sms, s);
 }
 
 }  // namespace
@@ -853,14 +869,13 @@ cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.M = p.T;
     g.N = p.I;
     g.kb = ceil_div(p.H, 64);
-    g.act = p.act;
     if (p.h) {
         g.out0 = p.h;
-        return launch_gemm<kFwd>(m, g, num_sms, s);
+        return launch_act<kFwd>(p.act, m, g, num_sms, s);
     }
     g.dh = p.dh;
     g.out0 = p.dgu;
-    return launch_gemm<kBwd>(m, g, num_sms, s);
+    return launch_act<kBwd>(p.act, m, g, num_sms, s);
 }
 
 cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
@@ -876,7 +891,7 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb_half = ceil_div(p.I, 64);
     g.kb = 2 * g.kb_half;
     g.out0 = p.dx;
-    return launch_gemm<kDx>(m, g, num_sms, s);
+    return launch_gemm<kDx, 0>(m, g, num_sms, s);
 }
 
 cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
@@ -892,7 +907,7 @@ cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb = ceil_div(p.T, 64);
     g.out0 = p.dwg;
     g.out1 = p.dwu;
-    return launch_gemm<kDw>(m, g, num_sms, s);
+    return launch_gemm<kDw, 0>(m, g, num_sms, s);
 }
 
 cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) {
@@ -922,7 +937,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.groups = num_sms / g.mt;
         if (g.groups < 1) g.groups = 1;
         if (g.groups > tiles) g.groups = tiles;
-        e = launch_small<kInner>(m, g, (int64_t)g.mt * g.groups, num_sms, s);
+        e = launch_small<kInner, 0>(m, g, (int64_t)g.mt * g.groups, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     if ((e = tc::map_matrix(&m.b0, p.w, p.N, p.K)) != cudaSuccess) return e;
@@ -930,7 +945,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     g.N = p.N;
     g.residual = p.residual;
     g.out0 = p.y;
-    return launch_gemm<kProj>(m, g, num_sms, s);
+    return launch_gemm<kProj, 0>(m, g, num_sms, s);
 }
 
 }  // namespace moe
