@@ -87,48 +87,75 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f32(uint32_t w) { return bf16_to_f32(w & 0xFFFFu); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+// W neighbouring BF16 (4: 8 bytes, 8: 16 bytes) as words.
+template <int W>
+struct Words {
+    uint32_t w[W / 2];
+};
+template <int W>
+__device__ __forceinline__ Words<W> load_words(const uint16_t *p) {
+    Words<W> r;
+    if (W == 8) {
+        const uint4 d = *reinterpret_cast<const uint4 *>(p);
+        r.w[0] = d.x, r.w[1] = d.y, r.w[W / 2 - 2] = d.z, r.w[W / 2 - 1] = d.w;
+    } else {
+        const uint2 d = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = d.x, r.w[1] = d.y;
+    }
+    return r;
+}
+template <int W>
+__device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[W]) {
+    if (W == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[W - 4], v[W - 3]),
+                                                   pack2(v[W - 2], v[W - 1]));
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 
-// Eight neighbouring outputs of one row: columns n .. n + 7 (all inside the
-// matrix: n and N are multiples of 8).  v: the sums (gated: g), u: gated only.
+// What the outputs at (row, n ..) need besides the sums: dh or the residual.
+template <int MODE, int W>
+__device__ __forceinline__ Words<W> side_words(const GemmArgs &g, int64_t row, int n) {
+    if (MODE == kBwd) return load_words<W>(g.dh + row * g.N + n);
+    if (MODE == kProj && g.residual) return load_words<W>(g.residual + row * g.N + n);
+    return Words<W>{};
+}
+
+// W neighbouring outputs of one row: columns n .. n + W - 1 (all inside the
+// matrix: n and N are multiples of W).  v: the sums (gated: g), u: gated only.
 // h, dg, du, dx, dW and y are rounded here, once, from FP32; dg and du are
 // BF16 because they are operands of the next products.
-template <int MODE, int ACT>
-__device__ __forceinline__ void finish8(const GemmArgs &g, int64_t row, int half, int n, const float (&v)[8],
-                                        const float (&u)[8]) {
-    float o[8];
+template <int MODE, int ACT, int W>
+__device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half, int n, const float (&v)[W],
+                                       const float (&u)[W], const Words<W> &side) {
+    float o[W];
     if (MODE == kFwd) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = act_value<ACT>(v[i]) * u[i];
-        *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(o);
+        for (int i = 0; i < W; ++i) o[i] = act_value<ACT>(v[i]) * u[i];
+        store_bf16<W>(g.out0 + row * g.N + n, o);
     } else if (MODE == kBwd) {
-        const uint4 d = *reinterpret_cast<const uint4 *>(g.dh + row * g.N + n);
-        const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
-        float p[8];
+        float p[W];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float dh = i & 1 ? hi_f32(dw[i >> 1]) : lo_f32(dw[i >> 1]);
+        for (int i = 0; i < W; ++i) {
+            const float dh = i & 1 ? hi_f32(side.w[i >> 1]) : lo_f32(side.w[i >> 1]);
             float a, da;
             act_value_grad<ACT>(v[i], a, da);
             o[i] = dh * u[i] * da;
             p[i] = dh * a;
         }
         uint16_t *r = g.out0 + row * 2 * g.N + n;
-        *reinterpret_cast<uint4 *>(r) = pack8(o);
-        *reinterpret_cast<uint4 *>(r + g.N) = pack8(p);
+        store_bf16<W>(r, o);
+        store_bf16<W>(r + g.N, p);
     } else if (MODE == kDw) {
-        *reinterpret_cast<uint4 *>((half ? g.out1 : g.out0) + row * g.N + n) = pack8(v);
+        store_bf16<W>((half ? g.out1 : g.out0) + row * g.N + n, v);
     } else {
+        // without a residual the words are zero; -0 + 0 is +0, so they are not added
         if (MODE == kProj && g.residual) {
-            const uint4 d = *reinterpret_cast<const uint4 *>(g.residual + row * g.N + n);
-            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = v[i] + (i & 1 ? hi_f32(dw[i >> 1]) : lo_f32(dw[i >> 1]));
-            *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(o);
+            for (int i = 0; i < W; ++i) o[i] = v[i] + (i & 1 ? hi_f32(side.w[i >> 1]) : lo_f32(side.w[i >> 1]));
+            store_bf16<W>(g.out0 + row * g.N + n, o);
         } else {
-            *reinterpret_cast<uint4 *>(g.out0 + row * g.N + n) = pack8(v);
+            store_bf16<W>(g.out0 + row * g.N + n, v);
         }
     }
 }
@@ -147,7 +174,7 @@ __device__ __forceinline__ void finish8(const GemmArgs &g, int64_t row, int half
 // are left out of the operand, and noted; the epilogue of a tile with such a
 // note adds v * b for exactly those elements to the rows that name the
 // adapter.  Non-finite v stays in its own row.
-struct AdapterSmem {
+struct __align__(16) AdapterSmem {
     int ids[256];    // of the tile's rows; -1: none
     int list[256];   // distinct ids
     int first[256];
@@ -183,11 +210,17 @@ __device__ __forceinline__ void list_adapters(AdapterSmem &s, const GemmArgs &g,
     }
     group_sync();
     for (int i = tid; i < rows; i += kGroup) {
+        // compared with every earlier row, four per load and no early way out
+        // (the loads of a scan that may stop wait for one another: 3 us)
         const int id = s.ids[i];
-        bool first = id >= 0;
-        // runs of one request end the search at once
-        for (int j = i - 1; j >= 0 && first; --j) first = s.ids[j] != id;
-        s.first[i] = first;
+        bool seen = id < 0;
+#pragma unroll 8
+        for (int j = 0; j < rows; j += 4) {
+            const int4 o = *reinterpret_cast<const int4 *>(s.ids + j);
+            seen |= (o.x == id && j < i) | (o.y == id && j + 1 < i) | (o.z == id && j + 2 < i) |
+                    (o.w == id && j + 3 < i);
+        }
+        s.first[i] = !seen;
     }
     group_sync();
     if (tid < 32) {
@@ -266,11 +299,11 @@ __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArg
 }
 
 // The terms that append_block left out, of row `row` with adapter id, added
-// to outputs n .. n + 7.
-__device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n, float *v) {
+// to outputs n .. n + w - 1.
+__device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n, float *v, int w) {
     const int id = g.ids[row];
     if (id < 0 || id >= g.n) return;
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < w; ++i)
         for (int j = 0; j < g.rank; ++j) {
             const uint16_t b = g.lora_b[((size_t)id * g.N + n + i) * g.rank + j];
             if ((b & 0x7F80u) == 0x7F80u) v[i] += bf16_to_f32(g.v[row * g.rank + j]) * bf16_to_f32(b);
@@ -506,8 +539,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                             fu[i] = gated(MODE) ? __uint_as_float(u[8 * q + i]) : 0.f;
                         }
                         if (MODE == kProj && adapters && *(volatile int *)&s_ad.bad)
-                            add_left_out(g, m, n + c + 8 * q, fv);
-                        finish8<MODE, ACT>(g, m, half, n + c + 8 * q, fv, fu);
+                            add_left_out(g, m, n + c + 8 * q, fv, 8);
+                        finish<MODE, ACT, 8>(g, m, half, n + c + 8 * q, fv, fu, side_words<MODE, 8>(g, m, n + c + 8 * q));
                     }
                 }
             }
@@ -716,48 +749,59 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         else
             __syncthreads();
         if (!s_abort) {
-            constexpr int per_row = gated(MODE) ? 8 : 16;  // groups of 8 outputs
+            // four outputs per thread: a warp reads 512 consecutive bytes of a part
+            constexpr int per_row = gated(MODE) ? 16 : 32;
             const int share = (rows + splits - 1) / splits;
             const int r0 = rank * share, r1 = min(rows, r0 + share);
             int bad = 0;
             if (MODE == kProj && adapters)
                 for (int q = 0; q < splits; ++q)
                     bad |= tc::ld_cluster(splits > 1 ? tc::map_rank(smem_u32(&s_ad.bad), q) : smem_u32(&s_ad.bad));
+#pragma unroll 2
             for (int i = threadIdx.x; i < (r1 - r0) * per_row; i += kSmallThreads) {
-                const int r = r0 + i / per_row, c = (i % per_row) * 8;
+                const int r = r0 + i / per_row, c = (i % per_row) * 4;
+                const int64_t row = (int64_t)m0 + r;
                 int id = 0;
+                Words<4> side = {};
                 if (MODE == kInner) {
                     const int slot = c / lines;
                     if (slot >= slots || part * 128 + c - slot * lines >= g.rank) continue;
                     id = s_ad.ids[r];
                     if (s_ad.list[a0 + slot] != id) continue;
-                } else if (n0 + c >= g.N) {
-                    continue;
+                } else {
+                    if (n0 + c >= g.N) continue;
+                    side = side_words<MODE, 4>(g, row, n0 + c);
                 }
-                float v[8] = {}, u[8] = {};
+                // four ranks' parts are requested before the first is added
+                // (a remote read takes about 0.4 us)
+                float v[4] = {}, u[4] = {};
                 const uint32_t at = smem + (uint32_t)(r * kPartPitch + c) * 4;
-                for (int q = 0; q < splits; ++q) {
-                    const uint32_t from = splits > 1 ? tc::map_rank(at, q) : at;
+                for (int q0 = 0; q0 < splits; q0 += 4) {
+                    float4 a[4], b[4];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float4 a = tc::ld_cluster16(from + 16 * j);
-                        v[4 * j] += a.x, v[4 * j + 1] += a.y, v[4 * j + 2] += a.z, v[4 * j + 3] += a.w;
-                        if (gated(MODE)) {
-                            const float4 b = tc::ld_cluster16(from + 256 + 16 * j);
-                            u[4 * j] += b.x, u[4 * j + 1] += b.y, u[4 * j + 2] += b.z, u[4 * j + 3] += b.w;
-                        }
+                    for (int q = 0; q < 4; ++q) {
+                        if (q0 + q >= splits) break;
+                        const uint32_t from = splits > 1 ? tc::map_rank(at, q0 + q) : at;
+                        a[q] = tc::ld_cluster16(from);
+                        if (gated(MODE)) b[q] = tc::ld_cluster16(from + 256);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (q0 + q >= splits) break;
+                        v[0] += a[q].x, v[1] += a[q].y, v[2] += a[q].z, v[3] += a[q].w;
+                        if (gated(MODE)) u[0] += b[q].x, u[1] += b[q].y, u[2] += b[q].z, u[3] += b[q].w;
                     }
                 }
                 if (MODE == kInner) {
                     const float sc = g.scale[id];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] *= sc;
+                    for (int j = 0; j < 4; ++j) v[j] *= sc;
                     // rounded to BF16: an operand of the projection's appended blocks
-                    *reinterpret_cast<uint4 *>(g.v + (size_t)(m0 + r) * g.rank + part * 128 + c % lines) = pack8(v);
+                    store_bf16<4>(g.v + (size_t)row * g.rank + part * 128 + c % lines, v);
                     continue;
                 }
-                if (MODE == kProj && bad) add_left_out(g, (int64_t)m0 + r, n0 + c, v);
-                finish8<MODE, ACT>(g, (int64_t)m0 + r, half, n0 + c, v, u);
+                if (MODE == kProj && bad) add_left_out(g, row, n0 + c, v, 4);
+                finish<MODE, ACT, 4>(g, row, half, n0 + c, v, u, side);
             }
         }
         if (MODE == kInner) tc::fence_async();  // the parts' space becomes stages again
@@ -813,7 +857,7 @@ cudaError_t launch_small(const Maps &m, const GemmArgs &g, int64_t tiles, int nu
     });
     if (e != cudaSuccess) return e;
     int splits = 1;
-    while (splits < kMaxSplits && tiles * splits < num_sms && 2 * splits <= g.kb / 2) splits *= 2;
+    while (splits < kMaxSplits && 2 * tiles * splits <= num_sms && 2 * splits <= g.kb / 2) splits *= 2;
     // one slot is for appended adapter blocks
     const int slots = tiles * splits > num_sms ? 3 : kSmallMaxStages;
     const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);

@@ -148,8 +148,7 @@ __device__ __forceinline__ float4 ld_cluster16(uint32_t a) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
+                 : "r"(a));
     return v;
 }
 // Arrivals on a barrier given by its cluster address.  arrive_tx announces a
