@@ -54,7 +54,9 @@ cudaError_t launch_rms_norm(const uint16_t *x, int T, int H, uint16_t *xn, cudaS
     return launch_ex(rms_norm_kernel, dim3(T), dim3(kThreads), 0, s, true, x, H, xn);
 }
 
-cudaError_t launch_gated(const GatedParams &p, int sms, cudaStream_t s) { return launch_gated_tc(p, sms, s); }
+cudaError_t launch_gated(const GatedParams &p, int sms, cudaStream_t s) {
+    return gemv_supported(p.T, p.H) ? launch_gated_gemv(p, sms, s) : launch_gated_tc(p, sms, s);
+}
 
 cudaError_t launch_gated_backward(const GatedParams &p, int sms, cudaStream_t s) {
     cudaError_t e = launch_gated_tc(p, sms, s);
@@ -64,9 +66,13 @@ cudaError_t launch_gated_backward(const GatedParams &p, int sms, cudaStream_t s)
 }
 
 size_t adapter_workspace(int T, int, int, int, int rank) {
-    return ((size_t)T * rank * sizeof(uint16_t) + 255) / 256 * 256;  // v in BF16
+    // v: FP32 of up to 8 tokens, else BF16
+    const size_t n = (size_t)T * rank * (T <= 8 ? sizeof(float) : sizeof(uint16_t));
+    return (n + 255) / 256 * 256;
 }
 
-cudaError_t launch_adapter_proj(const AdapterParams &p, int sms, cudaStream_t s) { return launch_proj_tc(p, sms, s); }
+cudaError_t launch_adapter_proj(const AdapterParams &p, int sms, cudaStream_t s) {
+    return gemv_supported(p.T, p.K) ? launch_proj_gemv(p, sms, s) : launch_proj_tc(p, sms, s);
+}
 
 }  // namespace moe

@@ -40,6 +40,10 @@ struct AdapterParams {
 cudaError_t launch_rms_norm(const uint16_t *x, int T, int H, uint16_t *xn, cudaStream_t s);
 cudaError_t launch_gated(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedParams &p, int num_sms, cudaStream_t s);
+// up to 8 tokens (dense_gemv.cu)
+bool gemv_supported(int T, int K);
+cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s);
 // tcgen05 products (dense_gemm.cu)
 cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s);
