@@ -381,7 +381,7 @@ def _ptr(t):
 def _out(t, like, shape, name, what, stream):
     """The caller's output tensor, checked, or a new one beside `like`."""
     if t is None:
-        t = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+        t = like.new_empty(shape)
         if stream is not None:
             t.record_stream(stream)
     else:
@@ -391,7 +391,7 @@ def _out(t, like, shape, name, what, stream):
 
 def _workspace(ws, need, like, name, stream):
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        ws = like.new_empty(need, dtype=torch.uint8)
         if stream is not None:
             ws.record_stream(stream)
     elif not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous():

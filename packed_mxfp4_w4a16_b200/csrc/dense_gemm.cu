@@ -267,8 +267,10 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
 // from `row0` of the list's rows on, matrix rows from m on) and `b` (128
 // output columns from n on), K-major with the 128-byte swizzle: 16-byte chunk
 // c of row r lies at r * 128 + 16 (c ^ (r & 7)).  One row of each per thread.
+// `a` has room for `rows` of them at least; `first`: v is read for the first
+// time, so kInner has to be waited for (B is fetched before).
 __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArgs &g, int e, int m, int row0,
-                                             int n, uint8_t *a, uint8_t *b, int tid) {
+                                             int n, int rows, uint8_t *a, uint8_t *b, int tid, bool first) {
     uint4 va[8], vb[8];
     const int id = s.ids[row0 + tid];
     const bool in = n + tid < g.N;
@@ -277,12 +279,16 @@ __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArg
         int at, col;
         chunk_of(e, c, g.rank, s.count, at, col);
         va[c] = vb[c] = make_uint4(0, 0, 0, 0);
-        if (at >= 0) {
-            const int ad = s.list[at];
-            if (ad == id) va[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
-            if (in)
-                vb[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)ad * g.N + n + tid) * g.rank + col));
-        }
+        if (at >= 0 && in)
+            vb[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)s.list[at] * g.N + n + tid) * g.rank + col));
+    }
+    if (first) pdl_wait();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        int at, col;
+        chunk_of(e, c, g.rank, s.count, at, col);
+        if (at >= 0 && s.list[at] == id)
+            va[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
     }
     bool bad = false;
 #pragma unroll
@@ -291,7 +297,7 @@ __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArg
                        w = non_finite(vb[c].w);
         bad |= (x | y | z | w) != 0;
         const uint32_t off = tid * 128 + 16 * (c ^ (tid & 7));
-        *reinterpret_cast<uint4 *>(a + off) = va[c];
+        if (tid < rows) *reinterpret_cast<uint4 *>(a + off) = va[c];
         *reinterpret_cast<uint4 *>(b + off) = make_uint4(vb[c].x & ~x, vb[c].y & ~y, vb[c].z & ~z, vb[c].w & ~w);
     }
     tc::fence_async();  // before the tensor core reads them
@@ -473,7 +479,6 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             uint8_t *xa = smem_raw + (smem - smem_u32(smem_raw)) + kBigStages * kBigStage, *xb = xa + 2 * tc::kBox;
             const uint32_t xfull = tc::map_rank(smem_u32(&s_xfull), 0);
             const uint32_t peer_bad = tc::map_rank(smem_u32(&s_ad.bad), rank ^ 1);
-            pdl_wait();
             int x = 0;
             bool ok = true;
 #pragma unroll 1
@@ -490,7 +495,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         if (!ok) break;
                     }
                     if (blocks) {
-                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, xa, xb, tid);
+                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, 128, xa, xb, tid, x == 0);
                         if (bad) {
                             s_ad.bad = 1;
                             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
@@ -549,6 +554,9 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             if (lane == 0) tc::arrive_cluster(buf ? empty1 : empty0);
         }
     }
+    // kInner may still run where no token had an adapter: whatever waits for
+    // this kernel relies on both being done
+    if (adapters) pdl_wait();
     __syncthreads();
     if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
     tc::fence_before();
@@ -568,22 +576,26 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 // memory, and each then finishes its share of the rows, adding the S parts in
 // rank order through distributed shared memory (the same bits every time, and
 // no workspace or counter that two calls could share).
-constexpr uint32_t kSmallStage = 4 * tc::kBox;
-constexpr int kSmallMaxStages = 6;
+// A stage holds one or two boxes of A (row tiles of up to 64, or 128 rows)
+// and two of B.
+constexpr int kSmallMaxStages = 8;
+constexpr uint32_t small_stage(int boxes) { return (2 + boxes) * tc::kBox; }
 constexpr int kSmallThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 adapters; all finish rows
 constexpr int kPartPitch = 132;     // floats per row of partial sums (528 bytes: spreads banks)
-static_assert(128 * kPartPitch * 4 <= 3 * kSmallStage, "the parts fit in three stages");
+constexpr size_t kParts = 128 * kPartPitch * 4;
 
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kSmallThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
-             const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits) {
+             const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits,
+             const int boxes) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSmallMaxStages], s_empty[kSmallMaxStages], s_done, s_xfull, s_xempty;
     __shared__ AdapterSmem s_ad;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t stage = (2 + boxes) * tc::kBox, b_at = boxes * tc::kBox;
     uint8_t *const base = smem_raw + (smem - smem_u32(smem_raw));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % splits, t = blockIdx.x / splits;
@@ -645,26 +657,27 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
         if (warp == 0) {
             if (lane == 0) {
-                const int boxes = rows > 64 ? 2 : 1;  // rows beyond are garbage that stays in its rows
-                const uint32_t bytes = boxes * tc::kBox + (MODE == kInner ? slots * lines * 128 : 2 * tc::kBox);
+                // boxes that hold rows; the rows beyond are garbage that stays in its rows
+                const int full = rows > 64 ? 2 : 1;
+                const uint32_t bytes = full * tc::kBox + (MODE == kInner ? slots * lines * 128 : 2 * tc::kBox);
                 bool ok = !*abort;
                 const int it0 = it;
 #pragma unroll 1
                 for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
                     const int s = it % stages;
                     if (it >= stages && !(ok = tc::wait(&s_empty[s], (it / stages - 1) & 1, abort))) break;
-                    const uint32_t bar = smem_u32(&s_full[s]), dst = smem + s * kSmallStage;
+                    const uint32_t bar = smem_u32(&s_full[s]), dst = smem + s * stage;
                     mbar_arrive_expect_tx(&s_full[s], bytes);
                     if (MODE == kInner) {
                         for (int i = 0; i < slots; ++i)
-                            load_b<MODE, 1>(dst + 2 * tc::kBox + i * lines * 128, &map_b0, &map_b1, g, kb,
+                            load_b<MODE, 1>(dst + b_at + i * lines * 128, &map_b0, &map_b1, g, kb,
                                             s_ad.list[a0 + i], part * 128, bar);
                     } else {
-                        load_b<MODE, 1>(dst + 2 * tc::kBox, &map_b0, &map_b1, g, kb, n0, 0, bar);
-                        load_b<MODE, 1>(dst + 3 * tc::kBox, &map_b0, &map_b1, g, kb, gated(MODE) ? n0 : n0 + 64, 1,
+                        load_b<MODE, 1>(dst + b_at, &map_b0, &map_b1, g, kb, n0, 0, bar);
+                        load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb, gated(MODE) ? n0 : n0 + 64, 1,
                                         bar);
                     }
-                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, boxes, bar);
+                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, full, bar);
                 }
                 if (!ok)
                     for (int j = it > it0 + stages ? it - stages : it0; j < it; ++j)
@@ -681,8 +694,8 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     const int s = it % stages;
                     if (!(ok = tc::wait(&s_full[s], (it / stages) & 1, abort))) break;
                     tc::fence_after();
-                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * kSmallStage);
-                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * kSmallStage + 2 * tc::kBox);
+                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * stage);
+                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * stage + b_at);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma<1>(tmem, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
@@ -695,8 +708,8 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         tc::fence_after();
                         const int cmd = *(volatile int *)&s_ad.cmd;
                         last = cmd & 2;
-                        const uint64_t da = tc::desc<false>(smem + stages * kSmallStage);
-                        const uint64_t db = tc::desc<false>(smem + stages * kSmallStage + 2 * tc::kBox);
+                        const uint64_t da = tc::desc<false>(smem + stages * stage);
+                        const uint64_t db = tc::desc<false>(smem + stages * stage + b_at);
                         if (cmd & 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, id, true);
@@ -709,16 +722,15 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             __syncwarp();
         } else if (MODE == kProj && warp >= 4 && adapters) {
             const int tid = threadIdx.x - 128;
-            pdl_wait();
             list_adapters(s_ad, g, m0, 128, tid);
             const int blocks = adapter_blocks(s_ad.count, g.rank);
             const int e0 = blocks * rank / splits, e1 = blocks * (rank + 1) / splits;
-            uint8_t *xa = base + stages * kSmallStage;
+            uint8_t *xa = base + stages * stage;
             int x = 0;
 #pragma unroll 1
             for (int e = e0; e < max(e1, e0 + 1); ++e, ++x) {
                 if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort))) break;
-                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, xa, xa + 2 * tc::kBox, tid)) s_ad.bad = 1;
+                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, rows, xa, xa + b_at, tid, x == 0)) s_ad.bad = 1;
                 if (tid == 0) s_ad.cmd = (e < e1 ? 1 : 0) | (e + 1 >= e1 ? 2 : 0);
                 group_sync();
                 if (tid == 0) mbar_arrive(&s_xfull);
@@ -811,6 +823,9 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         else
             __syncthreads();
     }
+    // kInner may still run where no token had an adapter: whatever waits for
+    // this kernel relies on both being done
+    if (adapters) pdl_wait();
     if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
     if (warp == 2) {
         tc::fence_after();
@@ -847,50 +862,91 @@ struct Maps {
 };
 
 constexpr int kMaxSplits = 8;  // portable cluster size
+constexpr size_t kSmallSmem = 200 * 1024;  // of one CTA's stages
+
+// Clusters that K is split over: until the SMs have a CTA each, with four K
+// blocks at least for every CTA.
+int splits_for(int64_t tiles, int kb, int num_sms) {
+    int splits = 1;
+    while (splits < kMaxSplits && 2 * tiles * splits <= num_sms && 2 * splits <= kb / 4) splits *= 2;
+    return splits;
+}
+
+// Pairs of CTAs (true) or single ones, by their estimated time.  Either way
+// an SM takes in 32 KB per K block of a tile.  Measured: 117 bytes per ns per
+// SM where the operands come from L2 (then a pair's products keep up, 0.28 us
+// per block), about 45 where every byte comes from HBM; the share between is
+// the matrices' bytes over all that is loaded.  A split K adds about 2 us for
+// the join.
+bool use_pairs(int mode, const GemmArgs &g, int num_sms) {
+    const int halves = mode == kDw ? 2 : 1, bn = gated(mode) ? 128 : 256;
+    if (g.M <= 128) return false;
+    const int64_t big = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, bn);
+    const int64_t small = (int64_t)ceil_div(g.M, 128) * halves * ceil_div(g.N, bn / 2);
+    const double once = 128.0 * g.kb * ((double)g.M * halves + (double)g.N * (gated(mode) ? 2 : 1));
+    auto time = [&](int64_t ctas, int splits) {
+        const double blocks = ceil_div(g.kb, splits), all = 32768.0 * blocks * (double)(ctas * splits);
+        const double share = once < all ? once / all : 1.0;
+        const double waves = (double)((ctas * splits + num_sms - 1) / num_sms);
+        return waves * blocks * 32.768 * (share / 45 + (1 - share) / 117) + (splits > 1 ? 2 : 0);
+    };
+    return time(2 * big, 1) < time(small, splits_for(small, g.kb, num_sms));
+}
 
 template <int MODE, int ACT>
-cudaError_t launch_small(const Maps &m, const GemmArgs &g, int64_t tiles, int num_sms, cudaStream_t s) {
+cudaError_t launch_small(const Maps &m, GemmArgs g, int num_sms, bool before_pairs, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
         return cudaFuncSetAttribute(small_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)(kSmallMaxStages * kSmallStage + 1024));
+                                    (int)kSmallSmem + 1024);
     });
     if (e != cudaSuccess) return e;
-    int splits = 1;
-    while (splits < kMaxSplits && 2 * tiles * splits <= num_sms && 2 * splits <= g.kb / 2) splits *= 2;
+    g.mt_half = ceil_div(g.M, 128);
+    g.mt = g.mt_half * (MODE == kDw ? 2 : 1);
+    int64_t tiles;
+    int splits;
+    if (MODE == kInner) {
+        tiles = (int64_t)g.mt * g.groups;
+        splits = splits_for(g.mt, g.kb, num_sms);
+    } else {
+        g.nt = ceil_div(g.N, gated(MODE) ? 64 : 128);
+        g.n_fast = g.nt < g.mt;
+        tiles = (int64_t)g.mt * g.nt;
+        splits = splits_for(tiles, g.kb, num_sms);
+    }
+    const int boxes = g.M > 64 ? 2 : 1;
+    const uint32_t stage = small_stage(boxes);
+    // Shared memory: one CTA on an SM with all the stages, or two with half
+    // where there are more CTAs than SMs.  kInner and the single-CTA projection
+    // after it share an SM, 1 to 2, so that the projection's K loop runs
+    // beside kInner.
+    size_t budget = tiles * splits > num_sms ? kSmallSmem / 2 : kSmallSmem;
+    if (MODE == kInner && !before_pairs) budget = kSmallSmem / 3 + 8192;
+    if (MODE == kProj && g.n > 0 && tiles * splits <= num_sms) budget = kSmallSmem / 3 * 2 + 16384;
+    int slots = (int)(budget / stage);
+    if (slots > kSmallMaxStages) slots = kSmallMaxStages;
     // one slot is for appended adapter blocks
-    const int slots = tiles * splits > num_sms ? 3 : kSmallMaxStages;
     const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);
-    return launch_cluster(small_kernel<MODE, ACT>, (unsigned)(tiles * splits), kSmallThreads,
-                          (size_t)slots * kSmallStage + 1024, splits > 1 ? splits : 0, s, m.a, m.b0, m.b1, g,
-                          stages, splits);
+    const size_t smem = (size_t)slots * stage > kParts ? (size_t)slots * stage : kParts;
+    return launch_cluster(small_kernel<MODE, ACT>, (unsigned)(tiles * splits), kSmallThreads, smem + 1024,
+                          splits > 1 ? splits : 0, s, m.a, m.b0, m.b1, g, stages, splits, boxes);
 }
 
 template <int MODE, int ACT>
 cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
+    if (!use_pairs(MODE, g, num_sms)) return launch_small<MODE, ACT>(m, g, num_sms, false, s);
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
         return cudaFuncSetAttribute(big_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
     });
     if (e != cudaSuccess) return e;
-    const int halves = MODE == kDw ? 2 : 1;
-    const int bn = gated(MODE) ? 128 : 256;
-    // Pairs of CTAs when their 256-row tiles fill the GPU; else single CTAs,
-    // K split over a cluster until the GPU is filled.
-    const int64_t big_tiles = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, bn);
-    if (g.M > 128 && big_tiles >= num_sms / 2) {
-        g.mt_half = ceil_div(g.M, 256);
-        g.mt = g.mt_half * halves;
-        g.nt = ceil_div(g.N, bn);
-        g.n_fast = g.nt < g.mt;
-        const int pairs = (int)(big_tiles < num_sms / 2 ? big_tiles : num_sms / 2);
-        return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
-    }
-    g.mt_half = ceil_div(g.M, 128);
-    g.mt = g.mt_half * halves;
-    g.nt = ceil_div(g.N, bn / 2);
+    g.mt_half = ceil_div(g.M, 256);
+    g.mt = g.mt_half * (MODE == kDw ? 2 : 1);
+    g.nt = ceil_div(g.N, gated(MODE) ? 128 : 256);
     g.n_fast = g.nt < g.mt;
-    return launch_small<MODE, ACT>(m, g, (int64_t)g.mt * g.nt, num_sms, s);
+    const int64_t tiles = (int64_t)g.mt * g.nt;
+    const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
 }
 
 template <int MODE>
@@ -968,25 +1024,28 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     g.v = reinterpret_cast<uint16_t *>(p.v);
     g.n = p.n;
     g.rank = p.rank;
+    g.N = p.N;
     if (p.n > 0) {
         const int lines = p.rank < 128 ? p.rank : 128;
         if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
         m.b1 = m.b0;
         g.per_tile = 128 / lines;
         g.parts = ceil_div(p.rank, 128);
-        g.mt = ceil_div(p.T, 128);
-        // as many clusters per row tile as its adapters could use, while they fit the GPU
+        // SMs that K splits leave go to clusters that share a row tile's
+        // adapters (a split always has work, such a cluster may find none),
+        // fewer adapters at a time if that gives each of them some
+        const int mt = ceil_div(p.T, 128), splits = splits_for(mt, g.kb, num_sms);
         const int most = p.n < 128 ? p.n : 128;
-        const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
-        g.groups = num_sms / g.mt;
+        g.groups = num_sms / (mt * splits);
         if (g.groups < 1) g.groups = 1;
+        while (g.per_tile > 1 && ceil_div(most, g.per_tile) < g.groups) g.per_tile = (g.per_tile + 1) / 2;
+        const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
         if (g.groups > tiles) g.groups = tiles;
-        e = launch_small<kInner, 0>(m, g, (int64_t)g.mt * g.groups, num_sms, s);
+        e = launch_small<kInner, 0>(m, g, num_sms, use_pairs(kProj, g, num_sms), s);
         if (e != cudaSuccess) return e;
     }
     if ((e = tc::map_matrix(&m.b0, p.w, p.N, p.K)) != cudaSuccess) return e;
     m.b1 = m.b0;
-    g.N = p.N;
     g.residual = p.residual;
     g.out0 = p.y;
     return launch_gemm<kProj, 0>(m, g, num_sms, s);

@@ -225,6 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
             }
         }
     }
+    // inner_kernel may still run where no token had an adapter: whatever waits
+    // for this kernel relies on both being done
+    if (late) pdl_wait();
     __syncthreads();
     if (threadIdx.x == 0 && s_abort) atomicOr(p.status, kTimeoutStatus);
 }
