@@ -33,6 +33,7 @@ struct GemmArgs {
     int kb, kb_half;           // K blocks of 64; kDx: of one half
     int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
     int n_fast;                // consecutive tiles share M (else N)
+    int width, cols;           // small_kernel: output columns per tile, columns of its products
     // adapters (kProj with n > 0, kInner)
     const int32_t *ids;        // [M]
     const float *scale;        // [n], kInner
@@ -267,13 +268,13 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
 // from `row0` of the list's rows on, matrix rows from m on) and `b` (128
 // output columns from n on), K-major with the 128-byte swizzle: 16-byte chunk
 // c of row r lies at r * 128 + 16 (c ^ (r & 7)).  One row of each per thread.
-// `a` has room for `rows` of them at least; `first`: v is read for the first
+// `a` has room for `lines` of them, `b` for `cols`; `first`: v is read for the first
 // time, so kInner has to be waited for (B is fetched before).
 __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArgs &g, int e, int m, int row0,
-                                             int n, int rows, uint8_t *a, uint8_t *b, int tid, bool first) {
+                                             int n, int lines, int cols, uint8_t *a, uint8_t *b, int tid, bool first) {
     uint4 va[8], vb[8];
     const int id = s.ids[row0 + tid];
-    const bool in = n + tid < g.N;
+    const bool in = tid < cols && n + tid < g.N;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         int at, col;
@@ -297,8 +298,9 @@ __device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArg
                        w = non_finite(vb[c].w);
         bad |= (x | y | z | w) != 0;
         const uint32_t off = tid * 128 + 16 * (c ^ (tid & 7));
-        if (tid < rows) *reinterpret_cast<uint4 *>(a + off) = va[c];
-        *reinterpret_cast<uint4 *>(b + off) = make_uint4(vb[c].x & ~x, vb[c].y & ~y, vb[c].z & ~z, vb[c].w & ~w);
+        if (tid < lines) *reinterpret_cast<uint4 *>(a + off) = va[c];
+        if (tid < cols)
+            *reinterpret_cast<uint4 *>(b + off) = make_uint4(vb[c].x & ~x, vb[c].y & ~y, vb[c].z & ~z, vb[c].w & ~w);
     }
     tc::fence_async();  // before the tensor core reads them
     return bad;
@@ -495,7 +497,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                         if (!ok) break;
                     }
                     if (blocks) {
-                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, 128, xa, xb, tid, x == 0);
+                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, 128, 128, xa, xb, tid, x == 0);
                         if (bad) {
                             s_ad.bad = 1;
                             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
@@ -568,18 +570,21 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 }
 
 // ------------------------------------------------------- small products --
-// One CTA (cta_group::1) owns 128 x 128 accumulators (gated: 64 columns of g
-// and the same 64 of u; kInner: the A rows of the adapters that fit in 128
-// columns, one tile after the other while the row tile names more of them).
+// One CTA (cta_group::1) owns up to 128 x 128 accumulators (gated: `width`
+// columns of g and the same of u; kInner: the A rows of the adapters that fit
+// in 128 columns, one tile after the other while the row tile names more of
+// them).  The width is chosen so that the tiles fill the SMs: a few hundred
+// tokens or fewer are bound by streaming the weights, and every SM that
+// streams adds its share.
 // Where the tiles are too few for the SMs, a cluster of S CTAs splits K (and
 // the appended adapter blocks): every CTA leaves its partial sums in shared
 // memory, and each then finishes its share of the rows, adding the S parts in
 // rank order through distributed shared memory (the same bits every time, and
 // no workspace or counter that two calls could share).
-// A stage holds one or two boxes of A (row tiles of up to 64, or 128 rows)
-// and two of B.
-constexpr int kSmallMaxStages = 8;
-constexpr uint32_t small_stage(int boxes) { return (2 + boxes) * tc::kBox; }
+// A stage holds `lines` (8 to 128) lines of 128 bytes of A and `cols` of B: the
+// fewer the tokens, the more stages of weights are in flight.
+constexpr int kSmallMaxStages = 16;
+__host__ __device__ constexpr uint32_t small_stage(int lines, int cols) { return (lines + cols) * 128; }
 constexpr int kSmallThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 adapters; all finish rows
 constexpr int kPartPitch = 132;     // floats per row of partial sums (528 bytes: spreads banks)
 constexpr size_t kParts = 128 * kPartPitch * 4;
@@ -588,14 +593,16 @@ template <int MODE, int ACT>
 __global__ void __launch_bounds__(kSmallThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
              const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits,
-             const int boxes) {
+             const int a_lines) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSmallMaxStages], s_empty[kSmallMaxStages], s_done, s_xfull, s_xempty;
     __shared__ AdapterSmem s_ad;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t stage = (2 + boxes) * tc::kBox, b_at = boxes * tc::kBox;
+    const uint32_t stage = small_stage(a_lines, g.cols), b_at = a_lines * 128;
+    // first product column of u
+    const int u_at = gated(MODE) ? g.cols / 2 : 0;
     uint8_t *const base = smem_raw + (smem - smem_u32(smem_raw));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % splits, t = blockIdx.x / splits;
@@ -621,10 +628,6 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     tc::fence_after();
     const uint32_t tmem = s_tmem;
     volatile int *abort = &s_abort;
-    // as in big_kernel, only v has to be waited for after kInner
-    const bool adapters = MODE == kProj && g.n > 0;
-    if (!adapters) pdl_wait();
-    pdl_launch_dependents();
 
     int mt, nt = 0;
     if (MODE == kInner) {
@@ -636,8 +639,12 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     }
     const int half = MODE == kDw && mt >= g.mt_half;
     if (half) mt -= g.mt_half;
-    const int m0 = mt * 128, n0 = nt * (gated(MODE) ? 64 : 128);
+    const int m0 = mt * 128, n0 = nt * g.width;
     const int kb0 = (int)((int64_t)g.kb * rank / splits), kb1 = (int)((int64_t)g.kb * (rank + 1) / splits);
+    // as in big_kernel, only v has to be waited for after kInner
+    const bool adapters = MODE == kProj && g.n > 0;
+    if (!adapters) pdl_wait();
+    pdl_launch_dependents();
     const int rows = min(128, g.M - m0);
     // kInner: this row tile's adapters, `per_tile` of them (or a part of one) at a time
     const int lines = MODE == kInner ? min(g.rank, 128) : 1;
@@ -657,9 +664,12 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
         if (warp == 0) {
             if (lane == 0) {
-                // boxes that hold rows; the rows beyond are garbage that stays in its rows
+                // boxes that hold rows; what the products read beyond is garbage that
+                // stays in its rows
                 const int full = rows > 64 ? 2 : 1;
-                const uint32_t bytes = full * tc::kBox + (MODE == kInner ? slots * lines * 128 : 2 * tc::kBox);
+                const uint32_t bytes = full * min(a_lines, 64) * 128 + (MODE == kInner  ? slots * lines * 128
+                                                          : gated(MODE) ? 2 * g.width * 128
+                                                                        : g.width * 128);
                 bool ok = !*abort;
                 const int it0 = it;
 #pragma unroll 1
@@ -673,9 +683,12 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                             load_b<MODE, 1>(dst + b_at + i * lines * 128, &map_b0, &map_b1, g, kb,
                                             s_ad.list[a0 + i], part * 128, bar);
                     } else {
+                        // K-major: `width` lines in one box; MN-major: boxes of 64 columns
                         load_b<MODE, 1>(dst + b_at, &map_b0, &map_b1, g, kb, n0, 0, bar);
-                        load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb, gated(MODE) ? n0 : n0 + 64, 1,
-                                        bar);
+                        if (gated(MODE))
+                            load_b<MODE, 1>(dst + b_at + u_at * 128, &map_b0, &map_b1, g, kb, n0, 1, bar);
+                        if (b_mn(MODE) && g.width > 64)
+                            load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb, n0 + 64, 0, bar);
                     }
                     load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, full, bar);
                 }
@@ -686,7 +699,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             __syncwarp();
         } else if (warp == 1) {
             if (lane == 0) {
-                constexpr uint32_t id = tc::idesc(128, 128, a_mn(MODE), b_mn(MODE));
+                const uint32_t id = tc::idesc(128, g.cols, a_mn(MODE), b_mn(MODE));
                 bool ok = !*abort;
                 int x = 0;
 #pragma unroll 1
@@ -730,7 +743,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 #pragma unroll 1
             for (int e = e0; e < max(e1, e0 + 1); ++e, ++x) {
                 if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort))) break;
-                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, rows, xa, xa + b_at, tid, x == 0)) s_ad.bad = 1;
+                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, a_lines, g.width, xa, xa + b_at, tid, x == 0)) s_ad.bad = 1;
                 if (tid == 0) s_ad.cmd = (e < e1 ? 1 : 0) | (e + 1 >= e1 ? 2 : 0);
                 group_sync();
                 if (tid == 0) mbar_arrive(&s_xfull);
@@ -740,20 +753,22 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const bool ok = tc::wait(&s_done, round & 1, abort);
         if (__syncthreads_and(ok)) {
             tc::fence_after();
-            // TMEM -> shared memory: warp w takes lanes 32 (w % 4) .., half of the columns
+            // TMEM -> shared memory: warp w takes lanes 32 (w % 4) .., every other
+            // 16 columns
             float *parts = reinterpret_cast<float *>(base);
             const int r = (warp & 3) * 32 + lane;
             const uint32_t acc = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            if ((warp & 3) * 32 < rows)
+#pragma unroll 2
+                for (int c = (warp >> 2) * 16; c < g.cols; c += 32) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(acc + c, v);
+                    tc::tmem_wait();
 #pragma unroll
-            for (int c = (warp >> 2) * 64; c < (warp >> 2) * 64 + 64; c += 16) {
-                uint32_t v[16];
-                tc::tmem_ld16(acc + c, v);
-                tc::tmem_wait();
-#pragma unroll
-                for (int q = 0; q < 16; q += 4)
-                    *reinterpret_cast<uint4 *>(parts + r * kPartPitch + c + q) =
-                        make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
-            }
+                    for (int q = 0; q < 16; q += 4)
+                        *reinterpret_cast<uint4 *>(parts + r * kPartPitch + c + q) =
+                            make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+                }
         }
         tc::fence_before();
         if (splits > 1)
@@ -761,59 +776,74 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         else
             __syncthreads();
         if (!s_abort) {
-            // four outputs per thread: a warp reads 512 consecutive bytes of a part
-            constexpr int per_row = gated(MODE) ? 16 : 32;
+            // Four outputs of a row at a time (a warp reads consecutive bytes of a
+            // part), four such groups per thread together: all that they read is
+            // requested before the first is added (a remote read takes about 0.4
+            // us, dh or the residual more).
+            const int per_row = MODE == kInner ? g.cols / 4 : g.width / 4;
             const int share = (rows + splits - 1) / splits;
             const int r0 = rank * share, r1 = min(rows, r0 + share);
             int bad = 0;
             if (MODE == kProj && adapters)
                 for (int q = 0; q < splits; ++q)
                     bad |= tc::ld_cluster(splits > 1 ? tc::map_rank(smem_u32(&s_ad.bad), q) : smem_u32(&s_ad.bad));
+            constexpr int U = 4;
+#pragma unroll 1
+            for (int i0 = threadIdx.x; i0 < (r1 - r0) * per_row; i0 += U * kSmallThreads) {
+                int row[U], col[U];
+                float scale[U];
+                Words<4> side[U];
+                float v[U][4] = {}, u[U][4] = {};
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int i = i0 + k * kSmallThreads;
+                    bool on = i < (r1 - r0) * per_row;
+                    const int r = r0 + i / per_row, c = (i % per_row) * 4;
+                    if (MODE == kInner) {
+                        const int slot = c / lines;
+                        on = on && slot < slots && part * 128 + c - slot * lines < g.rank;
+                        const int id = on ? s_ad.ids[r] : -1;
+                        on = on && s_ad.list[a0 + slot] == id;
+                        scale[k] = on ? g.scale[id] : 0.f;
+                    } else {
+                        on = on && n0 + c < g.N;
+                        if (on) side[k] = side_words<MODE, 4>(g, (int64_t)m0 + r, n0 + c);
+                    }
+                    row[k] = on ? r : -1;
+                    col[k] = c;
+                }
 #pragma unroll 2
-            for (int i = threadIdx.x; i < (r1 - r0) * per_row; i += kSmallThreads) {
-                const int r = r0 + i / per_row, c = (i % per_row) * 4;
-                const int64_t row = (int64_t)m0 + r;
-                int id = 0;
-                Words<4> side = {};
-                if (MODE == kInner) {
-                    const int slot = c / lines;
-                    if (slot >= slots || part * 128 + c - slot * lines >= g.rank) continue;
-                    id = s_ad.ids[r];
-                    if (s_ad.list[a0 + slot] != id) continue;
-                } else {
-                    if (n0 + c >= g.N) continue;
-                    side = side_words<MODE, 4>(g, row, n0 + c);
-                }
-                // four ranks' parts are requested before the first is added
-                // (a remote read takes about 0.4 us)
-                float v[4] = {}, u[4] = {};
-                const uint32_t at = smem + (uint32_t)(r * kPartPitch + c) * 4;
-                for (int q0 = 0; q0 < splits; q0 += 4) {
-                    float4 a[4], b[4];
+                for (int q = 0; q < splits; ++q) {
+                    const uint32_t from = splits > 1 ? tc::map_rank(smem, q) : smem;
+                    float4 a[U], b[U];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (q0 + q >= splits) break;
-                        const uint32_t from = splits > 1 ? tc::map_rank(at, q0 + q) : at;
-                        a[q] = tc::ld_cluster16(from);
-                        if (gated(MODE)) b[q] = tc::ld_cluster16(from + 256);
+                    for (int k = 0; k < U; ++k) {
+                        if (row[k] < 0) continue;
+                        const uint32_t at = from + (uint32_t)(row[k] * kPartPitch + col[k]) * 4;
+                        a[k] = tc::ld_cluster16(at);
+                        if (gated(MODE)) b[k] = tc::ld_cluster16(at + u_at * 4);
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (q0 + q >= splits) break;
-                        v[0] += a[q].x, v[1] += a[q].y, v[2] += a[q].z, v[3] += a[q].w;
-                        if (gated(MODE)) u[0] += b[q].x, u[1] += b[q].y, u[2] += b[q].z, u[3] += b[q].w;
+                    for (int k = 0; k < U; ++k) {
+                        if (row[k] < 0) continue;
+                        v[k][0] += a[k].x, v[k][1] += a[k].y, v[k][2] += a[k].z, v[k][3] += a[k].w;
+                        if (gated(MODE)) u[k][0] += b[k].x, u[k][1] += b[k].y, u[k][2] += b[k].z, u[k][3] += b[k].w;
                     }
                 }
-                if (MODE == kInner) {
-                    const float sc = g.scale[id];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] *= sc;
-                    // rounded to BF16: an operand of the projection's appended blocks
-                    store_bf16<4>(g.v + (size_t)row * g.rank + part * 128 + c % lines, v);
-                    continue;
+                for (int k = 0; k < U; ++k) {
+                    if (row[k] < 0) continue;
+                    const int64_t m = (int64_t)m0 + row[k];
+                    if (MODE == kInner) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[k][j] *= scale[k];
+                        // rounded to BF16: an operand of the projection's appended blocks
+                        store_bf16<4>(g.v + (size_t)m * g.rank + part * 128 + col[k] % lines, v[k]);
+                        continue;
+                    }
+                    if (MODE == kProj && bad) add_left_out(g, m, n0 + col[k], v[k], 4);
+                    finish<MODE, ACT, 4>(g, m, half, n0 + col[k], v[k], u[k], side[k]);
                 }
-                if (MODE == kProj && bad) add_left_out(g, row, n0 + c, v, 4);
-                finish<MODE, ACT, 4>(g, row, half, n0 + c, v, u, side);
             }
         }
         if (MODE == kInner) tc::fence_async();  // the parts' space becomes stages again
@@ -864,77 +894,144 @@ struct Maps {
 constexpr int kMaxSplits = 8;  // portable cluster size
 constexpr size_t kSmallSmem = 200 * 1024;  // of one CTA's stages
 
-// Clusters that K is split over: until the SMs have a CTA each, with four K
-// blocks at least for every CTA.
-int splits_for(int64_t tiles, int kb, int num_sms) {
-    int splits = 1;
-    while (splits < kMaxSplits && 2 * tiles * splits <= num_sms && 2 * splits <= kb / 4) splits *= 2;
-    return splits;
+// Lines of A in a stage of the single-CTA kernel: the rows there are (8-line
+// groups of the swizzle), 128 for more than 64.
+int a_lines(int mode, int M) { return M > 64 ? 128 : a_mn(mode) ? 64 : (M + 7) / 8 * 8; }
+
+// How many clusters of 2, 4 and 8 CTAs that fill an SM each can run at the
+// same time on the current device (GPCs have SMs that no cluster can use).
+struct ClusterFill {
+    int ctas[4];  // [log2 of the cluster's size]: CTAs
+};
+cudaError_t cluster_fill(int num_sms, ClusterFill *out);
+
+// What a launch does and its estimated time.
+struct Plan {
+    double us;
+    bool pairs;
+    int splits, width, cols, nt;
+};
+
+// Time of `ctas` CTAs that take `blocks` K blocks of `stage` bytes each, of
+// matrices of `once` bytes.  Measured: an SM takes in 117 bytes per ns where
+// the operands come from L2 (a pair's products keep up with that, 0.28 us per
+// block), about 45 where every byte comes from HBM; the share between is the
+// matrices' bytes over all that is loaded.
+double stream_us(int64_t ctas, int blocks, double stage, double once, int num_sms) {
+    const double all = stage * blocks * (double)ctas, share = once < all ? once / all : 1.0;
+    const double waves = (double)((ctas + num_sms - 1) / num_sms);
+    return waves * blocks * stage * 1e-3 * (share / 45 + (1 - share) / 117);
 }
 
-// Pairs of CTAs (true) or single ones, by their estimated time.  Either way
-// an SM takes in 32 KB per K block of a tile.  Measured: 117 bytes per ns per
-// SM where the operands come from L2 (then a pair's products keep up, 0.28 us
-// per block), about 45 where every byte comes from HBM; the share between is
-// the matrices' bytes over all that is loaded.  A split K adds about 2 us for
-// the join.
-bool use_pairs(int mode, const GemmArgs &g, int num_sms) {
-    const int halves = mode == kDw ? 2 : 1, bn = gated(mode) ? 128 : 256;
-    if (g.M <= 128) return false;
-    const int64_t big = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, bn);
-    const int64_t small = (int64_t)ceil_div(g.M, 128) * halves * ceil_div(g.N, bn / 2);
+// Pairs of CTAs with 256-row tiles, or single ones with a tile width and a
+// split of K; whichever the estimate prefers.
+Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill) {
+    const int halves = mode == kDw ? 2 : 1, most = gated(mode) ? 64 : 128;
     const double once = 128.0 * g.kb * ((double)g.M * halves + (double)g.N * (gated(mode) ? 2 : 1));
-    auto time = [&](int64_t ctas, int splits) {
-        const double blocks = ceil_div(g.kb, splits), all = 32768.0 * blocks * (double)(ctas * splits);
-        const double share = once < all ? once / all : 1.0;
-        const double waves = (double)((ctas * splits + num_sms - 1) / num_sms);
-        return waves * blocks * 32.768 * (share / 45 + (1 - share) / 117) + (splits > 1 ? 2 : 0);
-    };
-    return time(2 * big, 1) < time(small, splits_for(small, g.kb, num_sms));
+    Plan best = {1e30, true, 1, 0, 0, 0};
+    if (g.M > 128) {
+        const int64_t tiles = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, 2 * most);
+        best.us = stream_us(2 * tiles, g.kb, 4.0 * tc::kBox, once, num_sms / 2 * 2);
+    }
+    const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
+    // joining the parts of a split K: about 2 us, more for larger clusters
+    const double join[4] = {0, 1.5, 2, 3};
+    for (int l = 0; l < 4; ++l) {
+        const int splits = 1 << l;
+        if (l > 0 && g.kb / splits < 4) break;
+        Plan p = {0, false, splits, most, 0, 0};
+        const int64_t room = fill.ctas[l] / (mt * splits);  // tiles along N that run at once
+        if (b_mn(mode)) {
+            if (ceil_div(g.N, 64) <= room) p.width = 64;
+        } else if (room > ceil_div(g.N, most)) {
+            p.width = (ceil_div(g.N, room) + 3) / 4 * 4;
+            if (p.width < 8) p.width = 8;
+        }
+        p.cols = gated(mode) ? (p.width + 7) / 8 * 16 : (p.width + 15) / 16 * 16;
+        p.nt = ceil_div(g.N, p.width);
+        const double stage = small_stage(a_lines(mode, g.M), p.cols);
+        p.us = join[l] + stream_us(mt * p.nt * splits, ceil_div(g.kb, splits), stage, once, fill.ctas[l]);
+        if (p.us < best.us) best = p;
+    }
+    return best;
 }
 
 template <int MODE, int ACT>
-cudaError_t launch_small(const Maps &m, GemmArgs g, int num_sms, bool before_pairs, cudaStream_t s) {
+cudaError_t small_attribute() {
     static PerDeviceOnce once;
-    const cudaError_t e = per_device_once(once, [] {
+    return per_device_once(once, [] {
         return cudaFuncSetAttribute(small_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kSmallSmem + 1024);
     });
+}
+
+cudaError_t cluster_fill(int num_sms, ClusterFill *out) {
+    static PerDeviceOnce once;
+    static ClusterFill found[PerDeviceOnce::kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = per_device_once(once, [&] {
+        cudaError_t r = small_attribute<kDx, 0>();
+        ClusterFill f = {{num_sms, 0, 0, 0}};
+        for (int l = 1; l < 4 && r == cudaSuccess; ++l) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << l);
+            cfg.blockDim = dim3(kSmallThreads);
+            cfg.dynamicSmemBytes = kSmallSmem + 1024;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << l;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            r = cudaOccupancyMaxActiveClusters(&n, small_kernel<kDx, 0>, &cfg);
+            f.ctas[l] = n << l;
+        }
+        if (r == cudaSuccess) found[dev] = f;
+        return r;
+    });
+    if (e == cudaSuccess) *out = found[dev];
+    return e;
+}
+
+// `beside`: the launch and one after it are to share the SMs (kInner and the
+// single-CTA projection).
+template <int MODE, int ACT>
+cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sms, bool beside, cudaStream_t s) {
+    const cudaError_t e = small_attribute<MODE, ACT>();
     if (e != cudaSuccess) return e;
     g.mt_half = ceil_div(g.M, 128);
     g.mt = g.mt_half * (MODE == kDw ? 2 : 1);
-    int64_t tiles;
-    int splits;
-    if (MODE == kInner) {
-        tiles = (int64_t)g.mt * g.groups;
-        splits = splits_for(g.mt, g.kb, num_sms);
-    } else {
-        g.nt = ceil_div(g.N, gated(MODE) ? 64 : 128);
-        g.n_fast = g.nt < g.mt;
-        tiles = (int64_t)g.mt * g.nt;
-        splits = splits_for(tiles, g.kb, num_sms);
-    }
-    const int boxes = g.M > 64 ? 2 : 1;
-    const uint32_t stage = small_stage(boxes);
-    // Shared memory: one CTA on an SM with all the stages, or two with half
-    // where there are more CTAs than SMs.  kInner and the single-CTA projection
-    // after it share an SM, 1 to 2, so that the projection's K loop runs
-    // beside kInner.
-    size_t budget = tiles * splits > num_sms ? kSmallSmem / 2 : kSmallSmem;
-    if (MODE == kInner && !before_pairs) budget = kSmallSmem / 3 + 8192;
-    if (MODE == kProj && g.n > 0 && tiles * splits <= num_sms) budget = kSmallSmem / 3 * 2 + 16384;
-    int slots = (int)(budget / stage);
+    g.nt = plan.nt;
+    g.width = plan.width;
+    g.cols = plan.cols;
+    g.n_fast = g.nt < g.mt;
+    const int64_t ctas = (int64_t)g.mt * (MODE == kInner ? g.groups : g.nt) * plan.splits;
+    const int lines = a_lines(MODE, g.M);
+    const uint32_t stage = small_stage(lines, g.cols);
+    // Shared memory: one CTA on an SM with all the stages, or two with half of
+    // them where there are more CTAs than SMs; beside one another, a third for
+    // kInner and the rest for the projection, whose K loop then runs meanwhile.
+    size_t budget = ctas > num_sms ? kSmallSmem / 2 : kSmallSmem;
+    if (beside) budget = MODE == kInner ? kSmallSmem / 3 + 8192 : ctas > num_sms ? budget : kSmallSmem / 3 * 2 + 16384;
+    // the products read 128 rows of A also where a stage holds fewer: room
+    // behind the last stage keeps that inside the allocation
+    const size_t tail = 2 * tc::kBox - lines * 128;
+    int slots = (int)((budget - tail) / stage);
     if (slots > kSmallMaxStages) slots = kSmallMaxStages;
     // one slot is for appended adapter blocks
     const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);
-    const size_t smem = (size_t)slots * stage > kParts ? (size_t)slots * stage : kParts;
-    return launch_cluster(small_kernel<MODE, ACT>, (unsigned)(tiles * splits), kSmallThreads, smem + 1024,
-                          splits > 1 ? splits : 0, s, m.a, m.b0, m.b1, g, stages, splits, boxes);
+    size_t smem = (size_t)slots * stage + tail;
+    if (smem < kParts) smem = kParts;
+    return launch_cluster(small_kernel<MODE, ACT>, (unsigned)ctas, kSmallThreads, smem + 1024,
+                          plan.splits > 1 ? plan.splits : 0, s, m.a, m.b0, m.b1, g, stages, plan.splits, lines);
 }
 
 template <int MODE, int ACT>
-cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
-    if (!use_pairs(MODE, g, num_sms)) return launch_small<MODE, ACT>(m, g, num_sms, false, s);
+cudaError_t launch_big(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
         return cudaFuncSetAttribute(big_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
@@ -949,38 +1046,63 @@ cudaError_t launch_gemm(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) 
     return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
 }
 
+// Activations [rows][cols] as K-major operand A.
+cudaError_t map_tokens(CUtensorMap *m, const uint16_t *x, int64_t rows, int64_t cols) {
+    const int lines = a_lines(kFwd, (int)rows);
+    return tc::map_matrix(m, x, rows, cols, lines < 64 ? lines : 64);
+}
+
+// A weight [rows][cols] as K-major operand B: lines per box as the plan's kernel loads them.
+cudaError_t map_weight(CUtensorMap *m, const uint16_t *w, int64_t rows, int64_t cols, const Plan &plan) {
+    return tc::map_matrix(m, w, rows, cols, plan.pairs ? 64 : plan.width);
+}
+
+template <int MODE, int ACT>
+cudaError_t launch_gemm(const Maps &m, const GemmArgs &g, const Plan &plan, int num_sms, cudaStream_t s) {
+    if (plan.pairs) return launch_big<MODE, ACT>(m, g, num_sms, s);
+    return launch_small<MODE, ACT>(m, g, plan, num_sms, MODE == kProj && g.n > 0, s);
+}
+
 template <int MODE>
-cudaError_t launch_act(int act, const Maps &m, const GemmArgs &g, int num_sms, cudaStream_t s) {
-    if (act == MOE_ACT_SILU) return launch_gemm<MODE, MOE_ACT_SILU>(m, g, num_sms, s);
-    if (act == MOE_ACT_GELU) return launch_gemm<MODE, MOE_ACT_GELU>(m, g, num_sms, s);
-    return launch_gemm<MODE, MOE_ACT_GELU_TANH>(m, g, num_sms, s);
+cudaError_t launch_act(int act, const Maps &m, const GemmArgs &g, const Plan &plan, int num_sms, cudaStream_t s) {
+    if (act == MOE_ACT_SILU) return launch_gemm<MODE, MOE_ACT_SILU>(m, g, plan, num_sms, s);
+    if (act == MOE_ACT_GELU) return launch_gemm<MODE, MOE_ACT_GELU>(m, g, plan, num_sms, s);
+    return launch_gemm<MODE, MOE_ACT_GELU_TANH>(m, g, plan, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
-    Maps m;
-    cudaError_t e = tc::map_matrix(&m.a, p.x, p.T, p.H);
-    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
-    if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
+    ClusterFill fill;
+    cudaError_t e = cluster_fill(num_sms, &fill);
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
     g.M = p.T;
     g.N = p.I;
     g.kb = ceil_div(p.H, 64);
+    const Plan plan = make_plan(kFwd, g, num_sms, fill);
+    Maps m;
+    e = map_tokens(&m.a, p.x, p.T, p.H);
+    if (e == cudaSuccess) e = map_weight(&m.b0, p.wg, p.I, p.H, plan);
+    if (e == cudaSuccess) e = map_weight(&m.b1, p.wu, p.I, p.H, plan);
+    if (e != cudaSuccess) return e;
     if (p.h) {
         g.out0 = p.h;
-        return launch_act<kFwd>(p.act, m, g, num_sms, s);
+        return launch_act<kFwd>(p.act, m, g, plan, num_sms, s);
     }
     g.dh = p.dh;
     g.out0 = p.dgu;
-    return launch_act<kBwd>(p.act, m, g, num_sms, s);
+    return launch_act<kBwd>(p.act, m, g, plan, num_sms, s);
 }
 
 cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+    ClusterFill fill;
+    cudaError_t e = cluster_fill(num_sms, &fill);
+    if (e != cudaSuccess) return e;
     Maps m;
-    cudaError_t e = tc::map_halves(&m.a, p.dgu, p.T, p.I);
+    const int lines = a_lines(kDx, p.T);
+    e = tc::map_halves(&m.a, p.dgu, p.T, p.I, lines < 64 ? lines : 64);
     if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
     if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
     if (e != cudaSuccess) return e;
@@ -991,12 +1113,15 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb_half = ceil_div(p.I, 64);
     g.kb = 2 * g.kb_half;
     g.out0 = p.dx;
-    return launch_gemm<kDx, 0>(m, g, num_sms, s);
+    return launch_gemm<kDx, 0>(m, g, make_plan(kDx, g, num_sms, fill), num_sms, s);
 }
 
 cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+    ClusterFill fill;
+    cudaError_t e = cluster_fill(num_sms, &fill);
+    if (e != cudaSuccess) return e;
     Maps m;
-    cudaError_t e = tc::map_halves(&m.a, p.dgu, p.T, p.I);
+    e = tc::map_halves(&m.a, p.dgu, p.T, p.I);
     if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.x, p.T, p.H);
     if (e != cudaSuccess) return e;
     m.b1 = m.b0;
@@ -1007,25 +1132,31 @@ cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb = ceil_div(p.T, 64);
     g.out0 = p.dwg;
     g.out1 = p.dwu;
-    return launch_gemm<kDw, 0>(m, g, num_sms, s);
+    return launch_gemm<kDw, 0>(m, g, make_plan(kDw, g, num_sms, fill), num_sms, s);
 }
 
 cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) {
+    ClusterFill fill;
+    cudaError_t e = cluster_fill(num_sms, &fill);
+    if (e != cudaSuccess) return e;
     Maps m;
-    cudaError_t e = tc::map_matrix(&m.a, p.x, p.T, p.K);
+    e = map_tokens(&m.a, p.x, p.T, p.K);
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
     g.M = p.T;
-    g.kb = ceil_div(p.K, 64);
-    g.ids = p.ids;
-    g.scale = p.scale;
-    g.lora_b = p.b;
-    g.v = reinterpret_cast<uint16_t *>(p.v);
-    g.n = p.n;
-    g.rank = p.rank;
     g.N = p.N;
+    g.kb = ceil_div(p.K, 64);
+    // (the same plan with and without adapters: a token without one gets the
+    // plain projection's bits)
+    const Plan plan = make_plan(kProj, g, num_sms, fill);
     if (p.n > 0) {
+        g.ids = p.ids;
+        g.scale = p.scale;
+        g.lora_b = p.b;
+        g.v = reinterpret_cast<uint16_t *>(p.v);
+        g.n = p.n;
+        g.rank = p.rank;
         const int lines = p.rank < 128 ? p.rank : 128;
         if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
         m.b1 = m.b0;
@@ -1034,21 +1165,25 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         // SMs that K splits leave go to clusters that share a row tile's
         // adapters (a split always has work, such a cluster may find none),
         // fewer adapters at a time if that gives each of them some
-        const int mt = ceil_div(p.T, 128), splits = splits_for(mt, g.kb, num_sms);
+        const int mt = ceil_div(p.T, 128);
+        Plan inner = {0, false, 1, 128, 128, 1};
+        while (inner.splits < kMaxSplits && 2 * mt * inner.splits <= num_sms && g.kb / (2 * inner.splits) >= 4)
+            inner.splits *= 2;
         const int most = p.n < 128 ? p.n : 128;
-        g.groups = num_sms / (mt * splits);
+        g.groups = num_sms / (mt * inner.splits);
         if (g.groups < 1) g.groups = 1;
         while (g.per_tile > 1 && ceil_div(most, g.per_tile) < g.groups) g.per_tile = (g.per_tile + 1) / 2;
+        inner.cols = (g.per_tile * lines + 15) / 16 * 16;
         const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
         if (g.groups > tiles) g.groups = tiles;
-        e = launch_small<kInner, 0>(m, g, num_sms, use_pairs(kProj, g, num_sms), s);
+        e = launch_small<kInner, 0>(m, g, inner, num_sms, !plan.pairs, s);
         if (e != cudaSuccess) return e;
     }
-    if ((e = tc::map_matrix(&m.b0, p.w, p.N, p.K)) != cudaSuccess) return e;
+    if ((e = map_weight(&m.b0, p.w, p.N, p.K, plan)) != cudaSuccess) return e;
     m.b1 = m.b0;
     g.residual = p.residual;
     g.out0 = p.y;
-    return launch_gemm<kProj, 0>(m, g, num_sms, s);
+    return launch_gemm<kProj, 0>(m, g, plan, num_sms, s);
 }
 
 }  // namespace moe

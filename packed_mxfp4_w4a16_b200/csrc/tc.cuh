@@ -262,20 +262,20 @@ inline cudaError_t map_stack(CUtensorMap *m, const uint16_t *base, int64_t n, in
     const cuuint32_t box[3] = {64, (cuuint32_t)lines, 1};
     return make_map(m, base, 3, dims, strides, box);
 }
-// A row-major [rows][cols] BF16 matrix, boxes of 64 columns x 64 rows;
+// A row-major [rows][cols] BF16 matrix, boxes of 64 columns x `lines` rows;
 // elements outside the matrix read as zero.
-inline cudaError_t map_matrix(CUtensorMap *m, const uint16_t *base, int64_t rows, int64_t cols) {
+inline cudaError_t map_matrix(CUtensorMap *m, const uint16_t *base, int64_t rows, int64_t cols, int lines = 64) {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
-    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t box[2] = {64, (cuuint32_t)lines};
     return make_map(m, base, 2, dims, strides, box);
 }
 // [rows][2][cols]: the two halves of a row kept apart, so that a box past
 // the end of one half reads zeros and not the other half.
-inline cudaError_t map_halves(CUtensorMap *m, const uint16_t *base, int64_t rows, int64_t cols) {
+inline cudaError_t map_halves(CUtensorMap *m, const uint16_t *base, int64_t rows, int64_t cols, int lines = 64) {
     const cuuint64_t dims[3] = {(cuuint64_t)cols, 2, (cuuint64_t)rows};
     const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 4};
-    const cuuint32_t box[3] = {64, 1, 64};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)lines};
     return make_map(m, base, 3, dims, strides, box);
 }
 
