@@ -403,75 +403,98 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     };
 
     if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
+        tc::Ring at;
+        bool ok = true;
+        const bool issue = tc::elect();
+        const uint32_t bar0 = tc::map_rank(smem_u32(&s_full[0]), 0);
 #pragma unroll 1
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int m, half, n;
-                place(t, m, half, n);
-                m += rank * 128;
-                if (!gated(MODE)) n += rank * 128;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int m, half, n;
+            place(t, m, half, n);
+            m += rank * 128;
+            if (!gated(MODE)) n += rank * 128;
 #pragma unroll 1
-                for (int kb = 0; kb < g.kb; ++kb, ++it) {
-                    const int s = it % kBigStages;
-                    if (it >= kBigStages && !(ok = tc::wait(&s_empty[s], (it / kBigStages - 1) & 1, abort))) break;
-                    const uint32_t bar = tc::map_rank(smem_u32(&s_full[s]), 0), dst = smem + s * kBigStage;
+            for (int kb = 0; kb < g.kb; ++kb, at.next(kBigStages)) {
+                if (at.pass > 0) {
+                    ok = tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                }
+                if (issue) {
+                    const uint32_t bar = bar0 + 8 * at.slot, dst = smem + at.slot * kBigStage;
                     tc::arrive_tx_cluster(bar, kBigStage);
                     load_a<MODE, 2>(dst, &map_a, g, kb, m, half, 2, bar);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         load_b<MODE, 2>(dst + (2 + i) * tc::kBox, &map_b0, &map_b1, g, kb, n + 64 * i, rank, bar);
                 }
+                __syncwarp();
             }
-            // on the way out after a wait gave up: nothing of this CTA in
-            // flight (the leader's barriers count both CTAs' bytes)
-            if (!ok && rank == 0)
-                for (int j = it > kBigStages ? it - kBigStages : 0; j < it; ++j)
-                    mbar_wait(&s_full[j % kBigStages], (j / kBigStages) & 1);
         }
+        // on the way out after a wait gave up: nothing of this CTA in flight
+        // (the leader's barriers count both CTAs' bytes)
+        if (!ok && rank == 0)
+            for (uint32_t i = 0; i < (uint32_t)kBigStages; ++i)
+                if (at.pass > 0 || i < at.slot) mbar_wait(&s_full[i], (i < at.slot ? at.pass : at.pass - 1) & 1);
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t id = tc::idesc(256, 256, a_mn(MODE), b_mn(MODE));
-            int it = 0, j = 0, x = 0;
-            bool ok = true;
+            const uint64_t a0 = tc::desc<a_mn(MODE)>(smem), b0 = tc::desc<b_mn(MODE)>(smem + 2 * tc::kBox);
+            const bool issue = tc::elect();
+            tc::Ring at;
+            int j = 0, x = 0;
+            bool ok = true, any = false;
 #pragma unroll 1
             for (int t = pair; t < tiles && ok; t += pairs, ++j) {
                 const int buf = j & 1;
-                if (j >= 2 && !(ok = tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort))) break;
+                if (j >= 2) {
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort));
+                    if (!ok) break;
+                }
                 tc::fence_after();
 #pragma unroll 1
-                for (int kb = 0; kb < g.kb; ++kb, ++it) {
-                    const int s = it % kBigStages;
-                    if (!(ok = tc::wait(&s_full[s], (it / kBigStages) & 1, abort))) break;
+                for (int kb = 0; kb < g.kb; ++kb, at.next(kBigStages)) {
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_full[at.slot], at.pass & 1, abort));
+                    if (!ok) break;
                     tc::fence_after();
-                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * kBigStage);
-                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * kBigStage + 2 * tc::kBox);
+                    const uint64_t da = a0 + at.slot * (kBigStage >> 4), db = b0 + at.slot * (kBigStage >> 4);
+                    if (issue) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc::mma<2>(tmem + buf * 256, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
-                                   db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > 0 || k > 0);
-                    tc::commit<2>(&s_empty[s]);
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma<2>(tmem + buf * 256, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
+                                       db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > 0 || k > 0);
+                        tc::commit<2>(&s_empty[at.slot]);
+                    }
+                    __syncwarp();
+                    any = true;
                 }
                 if (MODE == kProj && adapters) {
                     for (bool last = false; ok && !last; ++x) {
-                        if (!(ok = tc::wait(&s_xfull, x & 1, abort))) break;
+                        ok = __all_sync(0xffffffffu, tc::wait<true>(&s_xfull, x & 1, abort));
+                        if (!ok) break;
                         tc::fence_after();
                         const int cmd = *(volatile int *)&s_ad.cmd;
                         last = cmd & 2;
-                        const uint64_t da = tc::desc<false>(smem + kBigStages * kBigStage);
-                        const uint64_t db = tc::desc<false>(smem + kBigStages * kBigStage + 2 * tc::kBox);
-                        if (cmd & 1)
+                        const uint64_t da = a0 + kBigStages * (kBigStage >> 4), db = b0 + kBigStages * (kBigStage >> 4);
+                        if (issue) {
+                            if (cmd & 1)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma<2>(tmem + buf * 256, da + 2 * k, db + 2 * k, id, true);
-                        tc::commit<2>(&s_xempty);
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma<2>(tmem + buf * 256, da + 2 * k, db + 2 * k, id, true);
+                            tc::commit<2>(&s_xempty);
+                        }
+                        __syncwarp();
                     }
                 }
-                if (ok) tc::commit<2>(&s_tfull[buf]);
+                if (ok && issue) tc::commit<2>(&s_tfull[buf]);
+                __syncwarp();
             }
-            if (!ok && it > 0) mbar_wait(&s_empty[(it - 1) % kBigStages], ((it - 1) / kBigStages) & 1);
+            // leaving early: the products issued so far have finished
+            if (!ok && any) {
+                const uint32_t last = at.slot ? at.slot - 1 : kBigStages - 1;
+                mbar_wait(&s_empty[last], (at.slot ? at.pass : at.pass - 1) & 1);
+            }
             if (!ok && x > 0) mbar_wait(&s_xempty, (x - 1) & 1);
         }
         __syncwarp();
@@ -656,28 +679,33 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         w1 = g.parts > 1 ? s_ad.count * g.parts : (s_ad.count + g.per_tile - 1) / g.per_tile;
         wstep = g.groups;
     }
-    int it = 0, round = 0;
+    tc::Ring at;
+    int round = 0;
 #pragma unroll 1
     for (int w = w0; w < w1; w += wstep, ++round) {
         const int part = MODE == kInner ? w % g.parts : 0;
         const int a0 = MODE == kInner ? w / g.parts * g.per_tile : 0;
         const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
         if (warp == 0) {
-            if (lane == 0) {
-                // boxes that hold rows; what the products read beyond is garbage that
-                // stays in its rows
-                const int full = rows > 64 ? 2 : 1;
-                const uint32_t bytes = full * min(a_lines, 64) * 128 + (MODE == kInner  ? slots * lines * 128
-                                                          : gated(MODE) ? 2 * g.width * 128
-                                                                        : g.width * 128);
-                bool ok = !*abort;
-                const int it0 = it;
+            // boxes that hold rows; what the products read beyond is garbage that
+            // stays in its rows
+            const int full = rows > 64 ? 2 : 1;
+            const uint32_t bytes = full * min(a_lines, 64) * 128 + (MODE == kInner  ? slots * lines * 128
+                                                                    : gated(MODE) ? 2 * g.width * 128
+                                                                                  : g.width * 128);
+            const bool issue = tc::elect();
+            bool ok = !*abort;
+            ok = __all_sync(0xffffffffu, ok);
+            uint32_t issued = 0;
 #pragma unroll 1
-                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                    const int s = it % stages;
-                    if (it >= stages && !(ok = tc::wait(&s_empty[s], (it / stages - 1) & 1, abort))) break;
-                    const uint32_t bar = smem_u32(&s_full[s]), dst = smem + s * stage;
-                    mbar_arrive_expect_tx(&s_full[s], bytes);
+            for (int kb = kb0; kb < kb1 && ok; ++kb, at.next(stages), ++issued) {
+                if (at.pass > 0) {
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort));
+                    if (!ok) break;
+                }
+                if (issue) {
+                    const uint32_t bar = smem_u32(&s_full[at.slot]), dst = smem + at.slot * stage;
+                    tc::arrive_tx(&s_full[at.slot], bytes);
                     if (MODE == kInner) {
                         for (int i = 0; i < slots; ++i)
                             load_b<MODE, 1>(dst + b_at + i * lines * 128, &map_b0, &map_b1, g, kb,
@@ -692,47 +720,58 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                     load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, full, bar);
                 }
-                if (!ok)
-                    for (int j = it > it0 + stages ? it - stages : it0; j < it; ++j)
-                        mbar_wait(&s_full[j % stages], (j / stages) & 1);
+                __syncwarp();
             }
+            if (!ok)  // nothing in flight on the way out
+                for (uint32_t i = 0, left = min(issued, (uint32_t)stages); i < left; ++i) {
+                    const uint32_t back = i + 1;  // slots before the current one
+                    const bool wrapped = back > at.slot;
+                    mbar_wait(&s_full[wrapped ? at.slot + stages - back : at.slot - back],
+                              (wrapped ? at.pass - 1 : at.pass) & 1);
+                }
             __syncwarp();
         } else if (warp == 1) {
-            if (lane == 0) {
-                const uint32_t id = tc::idesc(128, g.cols, a_mn(MODE), b_mn(MODE));
-                bool ok = !*abort;
-                int x = 0;
+            const uint32_t id = tc::idesc(128, g.cols, a_mn(MODE), b_mn(MODE));
+            const uint64_t da0 = tc::desc<a_mn(MODE)>(smem), db0 = tc::desc<b_mn(MODE)>(smem + b_at);
+            const bool issue = tc::elect();
+            bool ok = !*abort;
+            ok = __all_sync(0xffffffffu, ok);
+            int x = 0;
 #pragma unroll 1
-                for (int kb = kb0; kb < kb1 && ok; ++kb, ++it) {
-                    const int s = it % stages;
-                    if (!(ok = tc::wait(&s_full[s], (it / stages) & 1, abort))) break;
-                    tc::fence_after();
-                    const uint64_t da = tc::desc<a_mn(MODE)>(smem + s * stage);
-                    const uint64_t db = tc::desc<b_mn(MODE)>(smem + s * stage + b_at);
+            for (int kb = kb0; kb < kb1 && ok; ++kb, at.next(stages)) {
+                ok = __all_sync(0xffffffffu, tc::wait(&s_full[at.slot], at.pass & 1, abort));
+                if (!ok) break;
+                tc::fence_after();
+                const uint64_t da = da0 + at.slot * (stage >> 4), db = db0 + at.slot * (stage >> 4);
+                if (issue) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma<1>(tmem, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
                                    db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > kb0 || k > 0);
-                    tc::commit<1>(&s_empty[s]);
+                    tc::commit<1>(&s_empty[at.slot]);
                 }
-                if (MODE == kProj && adapters) {
-                    for (bool last = false; ok && !last; ++x) {
-                        if (!(ok = tc::wait(&s_xfull, x & 1, abort))) break;
-                        tc::fence_after();
-                        const int cmd = *(volatile int *)&s_ad.cmd;
-                        last = cmd & 2;
-                        const uint64_t da = tc::desc<false>(smem + stages * stage);
-                        const uint64_t db = tc::desc<false>(smem + stages * stage + b_at);
+                __syncwarp();
+            }
+            if (MODE == kProj && adapters) {
+                for (bool last = false; ok && !last; ++x) {
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_xfull, x & 1, abort));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const int cmd = *(volatile int *)&s_ad.cmd;
+                    last = cmd & 2;
+                    const uint64_t da = da0 + stages * (stage >> 4), db = db0 + stages * (stage >> 4);
+                    if (issue) {
                         if (cmd & 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) tc::mma<1>(tmem, da + 2 * k, db + 2 * k, id, true);
                         tc::commit<1>(&s_xempty);
                     }
+                    __syncwarp();
                 }
-                tc::commit<1>(&s_done);
-                if (!ok) mbar_wait(&s_done, round & 1);
             }
+            if (issue) tc::commit<1>(&s_done);
             __syncwarp();
+            if (!ok) mbar_wait(&s_done, round & 1);
         } else if (MODE == kProj && warp >= 4 && adapters) {
             const int tid = threadIdx.x - 128;
             list_adapters(s_ad, g, m0, 128, tid);

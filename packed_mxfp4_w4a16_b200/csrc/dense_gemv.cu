@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
                     if (!ok) break;
                 }
                 const uint32_t bytes = (uint32_t)min(p.chunk, p.K - c * p.chunk) * 2;
-                if (lane == 0) mbar_arrive_expect_tx(&s_full[s], nrows * bytes);
+                if (lane == 0) tc::arrive_tx(&s_full[s], nrows * bytes);
                 __syncwarp();
                 if (row) bulk_load(ring0 + s * slot + lane * pitch, row + c * p.chunk, bytes, &s_full[s]);
             }

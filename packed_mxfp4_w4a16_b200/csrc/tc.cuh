@@ -123,6 +123,27 @@ __device__ __forceinline__ void tmem_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  The warps that issue copies and MMAs
+// run their loops whole, with the issue under this predicate: loop counters,
+// addresses and descriptors stay in uniform registers (with the loop inside
+// one lane a K block of 4 MMAs took 745 clocks of issue, whatever its data).
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+
+// Position in a ring of `n` slots: the slot, and the parity of its passes.
+struct Ring {
+    uint32_t slot = 0, pass = 0;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++slot == n) {
+            slot = 0;
+            ++pass;
+        }
+    }
+};
+
 // ---------------------------------------------------------------- cluster --
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -162,6 +183,11 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ void arrive_release_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void arrive_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void arrive_tx_cluster(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
                  "r"(bytes)
@@ -181,11 +207,14 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 // Bounded wait on phase `parity` of *bar; gives up as well once *abort is
 // set, and sets it when it runs out.  kDenseSpin: an accumulator is waited
 // for over a whole K loop, so the bound is longer than a copy's.
+// CLUSTER: acquire what the other CTA's threads wrote (costs about 0.1 us
+// more per wait; copies and tensor-core work need none of it).
 constexpr int kDenseSpin = 1 << 22;
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
 #pragma unroll 1
     for (int i = 0; i < kDenseSpin; ++i) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
     *abort = 1;
