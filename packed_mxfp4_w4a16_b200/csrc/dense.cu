@@ -61,7 +61,7 @@ cudaError_t launch_gated(const GatedParams &p, int sms, cudaStream_t s) {
 cudaError_t launch_gated_backward(const GatedParams &p, int sms, cudaStream_t s) {
     cudaError_t e = launch_gated_tc(p, sms, s);
     if (e == cudaSuccess && p.dx) e = launch_dx_tc(p, sms, s);
-    if (e == cudaSuccess && p.dwg) e = launch_dw_tc(p, sms, s);
+    if (e == cudaSuccess && p.dwg) e = launch_dw_tc(p, p.dx != nullptr, sms, s);
     return e;
 }
 

@@ -47,7 +47,7 @@ cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s
 // tcgen05 products (dense_gemm.cu)
 cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s);
-cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_dw_tc(const GatedParams &p, bool after_dx, int num_sms, cudaStream_t s);
 cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s);
 
 size_t adapter_workspace(int T, int K, int N, int n, int rank);

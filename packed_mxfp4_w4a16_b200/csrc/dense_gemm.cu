@@ -39,6 +39,10 @@ struct GemmArgs {
     const float *scale;        // [n], kInner
     const uint16_t *lora_b;    // [n][N][rank], kProj
     uint16_t *v;               // [M][rank] BF16: written by kInner, read by kProj
+    // Set for the second of two launches that both depend on the one before
+    // them only (dx, then dW, after kBwd): it starts as the first leaves SMs
+    // free, which lets it start only after its own wait, and waits for it at its end.
+    int late;
     int n, rank;
     int per_tile, parts;       // kInner: adapters per 128 columns, or tiles per adapter
     int groups;                // kInner: CTAs (clusters) that share a row tile's adapters
@@ -264,43 +268,50 @@ __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
     return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// Appended block e into the operand tiles at `a` (this CTA's 128 rows, ids
-// from `row0` of the list's rows on, matrix rows from m on) and `b` (128
-// output columns from n on), K-major with the 128-byte swizzle: 16-byte chunk
-// c of row r lies at r * 128 + 16 (c ^ (r & 7)).  One row of each per thread.
-// `a` has room for `lines` of them, `b` for `cols`; `first`: v is read for the first
-// time, so kInner has to be waited for (B is fetched before).
-__device__ __forceinline__ bool append_block(const AdapterSmem &s, const GemmArgs &g, int e, int m, int row0,
-                                             int n, int lines, int cols, uint8_t *a, uint8_t *b, int tid, bool first) {
-    uint4 va[8], vb[8];
+// A thread's share of an appended block: row `tid` of the A operand (a token's
+// v) and of the B operand (an output's row of the adapters' B).  Fetched ahead
+// of the buffer being free; kInner is waited for before the first v is read.
+struct AppendRow {
+    uint4 a[8], b[8];
+};
+__device__ __forceinline__ void fetch_block(AppendRow &f, const AdapterSmem &s, const GemmArgs &g, int e, int m,
+                                            int row0, int n, int cols, int tid, bool first) {
     const int id = s.ids[row0 + tid];
     const bool in = tid < cols && n + tid < g.N;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         int at, col;
         chunk_of(e, c, g.rank, s.count, at, col);
-        va[c] = vb[c] = make_uint4(0, 0, 0, 0);
+        f.b[c] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && in)
-            vb[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)s.list[at] * g.N + n + tid) * g.rank + col));
+            f.b[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)s.list[at] * g.N + n + tid) * g.rank + col));
     }
     if (first) pdl_wait();
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
         int at, col;
         chunk_of(e, c, g.rank, s.count, at, col);
+        f.a[c] = make_uint4(0, 0, 0, 0);
         if (at >= 0 && s.list[at] == id)
-            va[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
+            f.a[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
     }
+}
+// Into the operand tiles at `a` (room for `lines` rows) and `b` (`cols`),
+// K-major with the 128-byte swizzle: 16-byte chunk c of row r lies at r * 128
+// + 16 (c ^ (r & 7)).  True if a non-finite element of B was left out.
+__device__ __forceinline__ bool append_block(const AppendRow &f, uint8_t *a, uint8_t *b, int lines, int cols,
+                                             int tid) {
     bool bad = false;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        const uint32_t x = non_finite(vb[c].x), y = non_finite(vb[c].y), z = non_finite(vb[c].z),
-                       w = non_finite(vb[c].w);
+        const uint32_t x = non_finite(f.b[c].x), y = non_finite(f.b[c].y), z = non_finite(f.b[c].z),
+                       w = non_finite(f.b[c].w);
         bad |= (x | y | z | w) != 0;
         const uint32_t off = tid * 128 + 16 * (c ^ (tid & 7));
-        if (tid < lines) *reinterpret_cast<uint4 *>(a + off) = va[c];
+        if (tid < lines) *reinterpret_cast<uint4 *>(a + off) = f.a[c];
         if (tid < cols)
-            *reinterpret_cast<uint4 *>(b + off) = make_uint4(vb[c].x & ~x, vb[c].y & ~y, vb[c].z & ~z, vb[c].w & ~w);
+            *reinterpret_cast<uint4 *>(b + off) =
+                make_uint4(f.b[c].x & ~x, f.b[c].y & ~y, f.b[c].z & ~z, f.b[c].w & ~w);
     }
     tc::fence_async();  // before the tensor core reads them
     return bad;
@@ -382,8 +393,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     // With adapters this kernel follows kInner, which lets it start only
     // after its own inputs were complete: just v, which kInner writes, has to
     // be waited for, and only by the warps that read it.
-    const bool adapters = MODE == kProj && g.n > 0;
-    if (!adapters) pdl_wait();
+    const bool adapters = MODE == kProj && g.n > 0, late = adapters || g.late;
+    if (!late) pdl_wait();
     pdl_launch_dependents();
 
     // tile -> first row of the pair's tile, half (kDw), first output column
@@ -512,24 +523,25 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 place(t, m, half, n);
                 list_adapters(s_ad, g, m, 256, tid);
                 const int blocks = adapter_blocks(s_ad.count, g.rank);
+                AppendRow f;
+                if (blocks)
+                    fetch_block(f, s_ad, g, 0, m + rank * 128, rank * 128, n + rank * 128, 128, tid, true);
 #pragma unroll 1
                 for (int e = 0; e < (blocks ? blocks : 1); ++e, ++x) {
                     if (x > 0) {
-                        const bool mine = tc::wait(&s_xempty, (x - 1) & 1, abort);
-                        ok = group_all(mine);  // the whole group goes on or leaves
+                        ok = group_all(tc::wait(&s_xempty, (x - 1) & 1, abort));  // the whole group goes on or leaves
                         if (!ok) break;
                     }
-                    if (blocks) {
-                        const bool bad = append_block(s_ad, g, e, m + rank * 128, rank * 128, n + rank * 128, 128, 128, xa, xb, tid, x == 0);
-                        if (bad) {
-                            s_ad.bad = 1;
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
-                        }
+                    if (blocks && append_block(f, xa, xb, 128, 128, tid)) {
+                        s_ad.bad = 1;
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
                     }
                     if (tid == 0) s_ad.cmd = (blocks ? 1 : 0) | (e + 1 >= blocks ? 2 : 0);
                     asm volatile("fence.acq_rel.cluster;" ::: "memory");
                     group_sync();
                     if (tid == 0) tc::arrive_release_cluster(xfull);
+                    if (e + 1 < blocks)
+                        fetch_block(f, s_ad, g, e + 1, m + rank * 128, rank * 128, n + rank * 128, 128, tid, false);
                 }
                 group_sync();  // the list is rebuilt for the next tile
             }
@@ -579,9 +591,9 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             if (lane == 0) tc::arrive_cluster(buf ? empty1 : empty0);
         }
     }
-    // kInner may still run where no token had an adapter: whatever waits for
-    // this kernel relies on both being done
-    if (adapters) pdl_wait();
+    // the launch before may still run: whatever waits for this one relies on
+    // both being done
+    if (late) pdl_wait();
     __syncthreads();
     if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
     tc::fence_before();
@@ -665,8 +677,8 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const int m0 = mt * 128, n0 = nt * g.width;
     const int kb0 = (int)((int64_t)g.kb * rank / splits), kb1 = (int)((int64_t)g.kb * (rank + 1) / splits);
     // as in big_kernel, only v has to be waited for after kInner
-    const bool adapters = MODE == kProj && g.n > 0;
-    if (!adapters) pdl_wait();
+    const bool adapters = MODE == kProj && g.n > 0, late = adapters || g.late;
+    if (!late) pdl_wait();
     pdl_launch_dependents();
     const int rows = min(128, g.M - m0);
     // kInner: this row tile's adapters, `per_tile` of them (or a part of one) at a time
@@ -772,20 +784,34 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (issue) tc::commit<1>(&s_done);
             __syncwarp();
             if (!ok) mbar_wait(&s_done, round & 1);
+        } else if ((MODE == kBwd || MODE == kProj) && warp == 3) {
+            // dh or the residual of the rows that this CTA finishes, into L2
+            const uint16_t *side = MODE == kBwd ? g.dh : g.residual;
+            const int share = (rows + splits - 1) / splits;
+            if (side)
+                for (int i = lane; i < share; i += 32) {
+                    const int r = rank * share + i;
+                    if (r < rows)
+                        for (int c = 0; c < g.width && n0 + c < g.N; c += 32)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(side + (int64_t)(m0 + r) * g.N + n0 + c));
+                }
         } else if (MODE == kProj && warp >= 4 && adapters) {
             const int tid = threadIdx.x - 128;
             list_adapters(s_ad, g, m0, 128, tid);
             const int blocks = adapter_blocks(s_ad.count, g.rank);
             const int e0 = blocks * rank / splits, e1 = blocks * (rank + 1) / splits;
             uint8_t *xa = base + stages * stage;
+            AppendRow f;
+            if (e0 < e1) fetch_block(f, s_ad, g, e0, m0, 0, n0, g.width, tid, true);
             int x = 0;
 #pragma unroll 1
             for (int e = e0; e < max(e1, e0 + 1); ++e, ++x) {
                 if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort))) break;
-                if (e < e1 && append_block(s_ad, g, e, m0, 0, n0, a_lines, g.width, xa, xa + b_at, tid, x == 0)) s_ad.bad = 1;
+                if (e < e1 && append_block(f, xa, xa + b_at, a_lines, g.width, tid)) s_ad.bad = 1;
                 if (tid == 0) s_ad.cmd = (e < e1 ? 1 : 0) | (e + 1 >= e1 ? 2 : 0);
                 group_sync();
                 if (tid == 0) mbar_arrive(&s_xfull);
+                if (e + 1 < e1) fetch_block(f, s_ad, g, e + 1, m0, 0, n0, g.width, tid, false);
             }
         }
         // every warp: the sums are complete (so all copies have been used too)
@@ -892,9 +918,9 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         else
             __syncthreads();
     }
-    // kInner may still run where no token had an adapter: whatever waits for
-    // this kernel relies on both being done
-    if (adapters) pdl_wait();
+    // the launch before may still run: whatever waits for this one relies on
+    // both being done
+    if (late) pdl_wait();
     if (threadIdx.x == 0 && s_abort) atomicOr(g.status, kTimeoutStatus);
     if (warp == 2) {
         tc::fence_after();
@@ -955,11 +981,13 @@ struct Plan {
 // matrices of `once` bytes.  Measured: an SM takes in 117 bytes per ns where
 // the operands come from L2 (a pair's products keep up with that, 0.28 us per
 // block), about 45 where every byte comes from HBM; the share between is the
-// matrices' bytes over all that is loaded.
+// matrices' bytes over all that is loaded.  However few its bytes, a block
+// takes 0.25 us of issue and waits.
 double stream_us(int64_t ctas, int blocks, double stage, double once, int num_sms) {
     const double all = stage * blocks * (double)ctas, share = once < all ? once / all : 1.0;
     const double waves = (double)((ctas + num_sms - 1) / num_sms);
-    return waves * blocks * stage * 1e-3 * (share / 45 + (1 - share) / 117);
+    const double block = stage * 1e-3 * (share / 45 + (1 - share) / 117);
+    return waves * blocks * (block > 0.25 ? block : 0.25);
 }
 
 // Pairs of CTAs with 256-row tiles, or single ones with a tile width and a
@@ -974,7 +1002,7 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
     }
     const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
     // joining the parts of a split K: about 2 us, more for larger clusters
-    const double join[4] = {0, 1.5, 2, 3};
+    const double join[4] = {0, 2.5, 3, 3.5};
     for (int l = 0; l < 4; ++l) {
         const int splits = 1 << l;
         if (l > 0 && g.kb / splits < 4) break;
@@ -999,8 +1027,7 @@ template <int MODE, int ACT>
 cudaError_t small_attribute() {
     static PerDeviceOnce once;
     return per_device_once(once, [] {
-        return cudaFuncSetAttribute(small_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)kSmallSmem + 1024);
+        return smem_attributes(small_kernel<MODE, ACT>, kSmallSmem + 1024);
     });
 }
 
@@ -1052,10 +1079,10 @@ cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sm
     const int lines = a_lines(MODE, g.M);
     const uint32_t stage = small_stage(lines, g.cols);
     // Shared memory: one CTA on an SM with all the stages, or two with half of
-    // them where there are more CTAs than SMs; beside one another, a third for
-    // kInner and the rest for the projection, whose K loop then runs meanwhile.
+    // them where there are more CTAs than SMs; beside one another, 70 KB for
+    // kInner and twice that for the projection, whose K loop then runs meanwhile.
     size_t budget = ctas > num_sms ? kSmallSmem / 2 : kSmallSmem;
-    if (beside) budget = MODE == kInner ? kSmallSmem / 3 + 8192 : ctas > num_sms ? budget : kSmallSmem / 3 * 2 + 16384;
+    if (beside) budget = MODE == kInner ? 70 * 1024 : ctas > num_sms ? 70 * 1024 : 140 * 1024;
     // the products read 128 rows of A also where a stage holds fewer: room
     // behind the last stage keeps that inside the allocation
     const size_t tail = 2 * tc::kBox - lines * 128;
@@ -1073,7 +1100,7 @@ template <int MODE, int ACT>
 cudaError_t launch_big(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
-        return cudaFuncSetAttribute(big_kernel<MODE, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBigSmem);
+        return smem_attributes(big_kernel<MODE, ACT>, kBigSmem);
     });
     if (e != cudaSuccess) return e;
     g.mt_half = ceil_div(g.M, 256);
@@ -1155,7 +1182,7 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     return launch_gemm<kDx, 0>(m, g, make_plan(kDx, g, num_sms, fill), num_sms, s);
 }
 
-cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
+cudaError_t launch_dw_tc(const GatedParams &p, bool after_dx, int num_sms, cudaStream_t s) {
     ClusterFill fill;
     cudaError_t e = cluster_fill(num_sms, &fill);
     if (e != cudaSuccess) return e;
@@ -1171,6 +1198,7 @@ cudaError_t launch_dw_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb = ceil_div(p.T, 64);
     g.out0 = p.dwg;
     g.out1 = p.dwu;
+    g.late = after_dx;
     return launch_gemm<kDw, 0>(m, g, make_plan(kDw, g, num_sms, fill), num_sms, s);
 }
 

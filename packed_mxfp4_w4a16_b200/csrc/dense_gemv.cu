@@ -293,7 +293,7 @@ template <bool GATED, int ACT>
 cudaError_t launch_gemv(GemvArgs g, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
-        return cudaFuncSetAttribute(gemv_kernel<GATED, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+        return smem_attributes(gemv_kernel<GATED, ACT>, kSmemMost);
     });
     if (e != cudaSuccess) return e;
     if (!ring_plan(g.T, g.K, &g.ring, &g.chunk)) return cudaErrorInvalidValue;
@@ -330,8 +330,10 @@ cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s)
 
 cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s) {
     if (p.n > 0) {
-        const cudaError_t e =
-            launch_ex(inner_kernel, dim3(p.T * p.rank), dim3(kInnerThreads), 0, s, true, p);
+        static PerDeviceOnce once;
+        cudaError_t e = per_device_once(once, [] { return smem_attributes(inner_kernel, 0); });
+        if (e != cudaSuccess) return e;
+        e = launch_ex(inner_kernel, dim3(p.T * p.rank), dim3(kInnerThreads), 0, s, true, p);
         if (e != cudaSuccess) return e;
     }
     GemvArgs g = {};

@@ -35,6 +35,18 @@ inline cudaError_t per_device_once(PerDeviceOnce &o, F &&set) {
     return e;
 }
 
+// Dynamic shared-memory limit of a kernel, and the largest shared-memory share
+// of the SM while it runs: an SM changes that share only when it is idle, so
+// kernels that are to run beside one another must all prefer the same.
+template <typename F>
+inline cudaError_t smem_attributes(F *kernel, size_t bytes) {
+    const cudaError_t e =
+        bytes ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
+}
+
 constexpr int kDecodeMaxT = 4;      // tokens handled by the per-(token,slot) GEMV path
 constexpr int kMaxTopK = 8;
 constexpr int kGemvThreads = 512;   // gate/up GEMV: 16 warps, one CTA per SM
