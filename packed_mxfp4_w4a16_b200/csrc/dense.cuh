@@ -44,6 +44,7 @@ cudaError_t launch_gated_backward(const GatedParams &p, int num_sms, cudaStream_
 bool gemv_supported(int T, int K);
 cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s);
+cudaError_t launch_inner(const AdapterParams &p, bool bf16, int num_sms, cudaStream_t s);
 // tcgen05 products (dense_gemm.cu)
 cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s);

@@ -44,6 +44,7 @@ struct GemmArgs {
     // free, which lets it start only after its own wait, and waits for it at its end.
     int late;
     int n, rank;
+    int direct;                // small_kernel adds v B^T as it finishes rows
     int per_tile, parts;       // kInner: adapters per 128 columns, or tiles per adapter
     int groups;                // kInner: CTAs (clusters) that share a row tile's adapters
 };
@@ -327,6 +328,33 @@ __device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n,
             const uint16_t b = g.lora_b[((size_t)id * g.N + n + i) * g.rank + j];
             if ((b & 0x7F80u) == 0x7F80u) v[i] += bf16_to_f32(g.v[row * g.rank + j]) * bf16_to_f32(b);
         }
+}
+
+// v B^T of row `row`, added to outputs n .. n + 3 (the form for few tokens: a
+// row reads the B rows of its own adapter only, from L2).
+__device__ __forceinline__ void add_direct(const GemmArgs &g, int64_t row, int n, float (&acc)[4]) {
+    const int id = g.ids[row];
+    if (id < 0 || id >= g.n) return;
+    const uint4 *v = reinterpret_cast<const uint4 *>(g.v + row * g.rank);
+    const uint4 *b = reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)id * g.N + n) * g.rank);
+    const int chunks = g.rank / 8;
+#pragma unroll 2
+    for (int c = 0; c < chunks; ++c) {
+        const uint4 vv = v[c];
+        uint4 bv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bv[i] = __ldg(b + i * chunks + c);
+        const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t bw[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                acc[i] = fmaf(lo_f32(vw[h]), lo_f32(bw[h]), acc[i]);
+                acc[i] = fmaf(hi_f32(vw[h]), hi_f32(bw[h]), acc[i]);
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------- large products --
@@ -678,6 +706,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const int kb0 = (int)((int64_t)g.kb * rank / splits), kb1 = (int)((int64_t)g.kb * (rank + 1) / splits);
     // as in big_kernel, only v has to be waited for after kInner
     const bool adapters = MODE == kProj && g.n > 0, late = adapters || g.late;
+    const bool append = adapters && !g.direct;
     if (!late) pdl_wait();
     pdl_launch_dependents();
     const int rows = min(128, g.M - m0);
@@ -764,7 +793,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
                 __syncwarp();
             }
-            if (MODE == kProj && adapters) {
+            if (MODE == kProj && append) {
                 for (bool last = false; ok && !last; ++x) {
                     ok = __all_sync(0xffffffffu, tc::wait(&s_xfull, x & 1, abort));
                     if (!ok) break;
@@ -795,6 +824,18 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         for (int c = 0; c < g.width && n0 + c < g.N; c += 32)
                             asm volatile("prefetch.global.L2 [%0];" ::"l"(side + (int64_t)(m0 + r) * g.N + n0 + c));
                 }
+        } else if (MODE == kProj && warp >= 4 && adapters && g.direct) {
+            // B of the adapters of the rows that this CTA finishes, into L2: the
+            // tile's outputs are consecutive in it
+            const int share = (rows + splits - 1) / splits, r0 = rank * share;
+            const int bytes = min(g.width, g.N - n0) * g.rank * 2;
+            for (int i = threadIdx.x - 128; i < share * 32; i += 128) {
+                const int r = r0 + i / 32, id = r < rows ? g.ids[m0 + r] : -1;
+                if (id >= 0 && id < g.n)
+                    for (int b = i % 32 * 128; b < bytes; b += 32 * 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            reinterpret_cast<const uint8_t *>(g.lora_b + ((size_t)id * g.N + n0) * g.rank) + b));
+            }
         } else if (MODE == kProj && warp >= 4 && adapters) {
             const int tid = threadIdx.x - 128;
             list_adapters(s_ad, g, m0, 128, tid);
@@ -849,9 +890,10 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const int share = (rows + splits - 1) / splits;
             const int r0 = rank * share, r1 = min(rows, r0 + share);
             int bad = 0;
-            if (MODE == kProj && adapters)
+            if (MODE == kProj && append)
                 for (int q = 0; q < splits; ++q)
                     bad |= tc::ld_cluster(splits > 1 ? tc::map_rank(smem_u32(&s_ad.bad), q) : smem_u32(&s_ad.bad));
+            if (MODE == kProj && g.direct) pdl_wait();  // v
             constexpr int U = 4;
 #pragma unroll 1
             for (int i0 = threadIdx.x; i0 < (r1 - r0) * per_row; i0 += U * kSmallThreads) {
@@ -906,6 +948,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         store_bf16<4>(g.v + (size_t)m * g.rank + part * 128 + col[k] % lines, v[k]);
                         continue;
                     }
+                    if (MODE == kProj && g.direct) add_direct(g, m, n0 + col[k], v[k]);
                     if (MODE == kProj && bad) add_left_out(g, m, n0 + col[k], v[k], 4);
                     finish<MODE, ACT, 4>(g, m, half, n0 + col[k], v[k], u[k], side[k]);
                 }
@@ -1082,14 +1125,14 @@ cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sm
     // them where there are more CTAs than SMs; beside one another, 70 KB for
     // kInner and twice that for the projection, whose K loop then runs meanwhile.
     size_t budget = ctas > num_sms ? kSmallSmem / 2 : kSmallSmem;
-    if (beside) budget = MODE == kInner ? 70 * 1024 : ctas > num_sms ? 70 * 1024 : 140 * 1024;
+    if (beside && !g.direct) budget = MODE == kInner ? 70 * 1024 : ctas > num_sms ? 70 * 1024 : 140 * 1024;
     // the products read 128 rows of A also where a stage holds fewer: room
     // behind the last stage keeps that inside the allocation
     const size_t tail = 2 * tc::kBox - lines * 128;
     int slots = (int)((budget - tail) / stage);
     if (slots > kSmallMaxStages) slots = kSmallMaxStages;
     // one slot is for appended adapter blocks
-    const int stages = slots - (MODE == kProj && g.n > 0 ? 1 : 0);
+    const int stages = slots - (MODE == kProj && g.n > 0 && !g.direct ? 1 : 0);
     size_t smem = (size_t)slots * stage + tail;
     if (smem < kParts) smem = kParts;
     return launch_cluster(small_kernel<MODE, ACT>, (unsigned)ctas, kSmallThreads, smem + 1024,
@@ -1224,27 +1267,39 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.v = reinterpret_cast<uint16_t *>(p.v);
         g.n = p.n;
         g.rank = p.rank;
-        const int lines = p.rank < 128 ? p.rank : 128;
-        if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
-        m.b1 = m.b0;
-        g.per_tile = 128 / lines;
-        g.parts = ceil_div(p.rank, 128);
-        // SMs that K splits leave go to clusters that share a row tile's
-        // adapters (a split always has work, such a cluster may find none),
-        // fewer adapters at a time if that gives each of them some
-        const int mt = ceil_div(p.T, 128);
-        Plan inner = {0, false, 1, 128, 128, 1};
-        while (inner.splits < kMaxSplits && 2 * mt * inner.splits <= num_sms && g.kb / (2 * inner.splits) >= 4)
-            inner.splits *= 2;
-        const int most = p.n < 128 ? p.n : 128;
-        g.groups = num_sms / (mt * inner.splits);
-        if (g.groups < 1) g.groups = 1;
-        while (g.per_tile > 1 && ceil_div(most, g.per_tile) < g.groups) g.per_tile = (g.per_tile + 1) / 2;
-        inner.cols = (g.per_tile * lines + 15) / 16 * 16;
-        const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
-        if (g.groups > tiles) g.groups = tiles;
-        e = launch_small<kInner, 0>(m, g, inner, num_sms, !plan.pairs, s);
-        if (e != cudaSuccess) return e;
+        // Few tokens: inner products by plain loads, 1.25 x 2 T rank K bytes
+        // through L2 (about 8 TB/s), and v B^T as the rows are finished, 2 x
+        // width rank bytes per row of a CTA (about 64 per clock).  Otherwise both
+        // on the tensor cores.
+        const double inner_us = 2.5 * p.T * (double)p.rank * p.K / 8e6;
+        const double rows = (p.T < 128 ? p.T : 128) / (double)plan.splits;
+        const double add_us = rows * plan.width * 2 * p.rank / 64 / 1900;
+        g.direct = !plan.pairs && add_us < 2;
+        if (!plan.pairs && inner_us < 8) {
+            if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
+        } else {
+            const int lines = p.rank < 128 ? p.rank : 128;
+            if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
+            m.b1 = m.b0;
+            g.per_tile = 128 / lines;
+            g.parts = ceil_div(p.rank, 128);
+            // SMs that K splits leave go to clusters that share a row tile's
+            // adapters (a split always has work, such a cluster may find none),
+            // fewer adapters at a time if that gives each of them some
+            const int mt = ceil_div(p.T, 128);
+            Plan inner = {0, false, 1, 128, 128, 1};
+            while (inner.splits < kMaxSplits && 2 * mt * inner.splits <= num_sms && g.kb / (2 * inner.splits) >= 4)
+                inner.splits *= 2;
+            const int most = p.n < 128 ? p.n : 128;
+            g.groups = num_sms / (mt * inner.splits);
+            if (g.groups < 1) g.groups = 1;
+            while (g.per_tile > 1 && ceil_div(most, g.per_tile) < g.groups) g.per_tile = (g.per_tile + 1) / 2;
+            inner.cols = (g.per_tile * lines + 15) / 16 * 16;
+            const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
+            if (g.groups > tiles) g.groups = tiles;
+            e = launch_small<kInner, 0>(m, g, inner, num_sms, !plan.pairs, s);
+            if (e != cudaSuccess) return e;
+        }
     }
     if ((e = map_weight(&m.b0, p.w, p.N, p.K, plan)) != cudaSuccess) return e;
     m.b1 = m.b0;

@@ -232,40 +232,69 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
     if (threadIdx.x == 0 && s_abort) atomicOr(p.status, kTimeoutStatus);
 }
 
-// One CTA per (rank column, token).
-constexpr int kInnerThreads = 256;
+// Inner products of few tokens: one CTA per token and RJ rank rows of its
+// adapter (x is read once for all RJ), 16-byte loads, FP32 sums.  Tokens of the
+// same adapter read its rows through L2 again; from about 8 us of that on the
+// tensor-core form is the faster one.
+constexpr int kInnerThreads = 128;
+template <int RJ, bool BF16>
 __global__ void __launch_bounds__(kInnerThreads)
 inner_kernel(const AdapterParams p) {
-    __shared__ float red[kInnerThreads / 32];
+    __shared__ float red[kInnerThreads / 32][RJ];
     pdl_wait();
     pdl_launch_dependents();
-    const int j = blockIdx.x % p.rank, t = blockIdx.x / p.rank, id = p.ids[t];
+    const int groups = (p.rank + RJ - 1) / RJ;
+    const int j0 = blockIdx.x % groups * RJ, t = blockIdx.x / groups, id = p.ids[t];
     if (id < 0 || id >= p.n) {
-        if (threadIdx.x == 0 && j == 0 && id != -1) atomicOr(p.status, kBadAdapterStatus);
+        if (threadIdx.x == 0 && j0 == 0 && id != -1) atomicOr(p.status, kBadAdapterStatus);
         return;  // v of a token without an adapter is not read
     }
     const uint4 *x = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.K);
-    const uint4 *a = reinterpret_cast<const uint4 *>(p.a + ((size_t)id * p.rank + j) * p.K);
-    float s = 0.f;
-#pragma unroll 4
-    for (int c = threadIdx.x; c < p.K / 8; c += kInnerThreads) {
-        const uint4 xv = __ldg(x + c), av = __ldg(a + c);
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, aw[4] = {av.x, av.y, av.z, av.w};
+    const uint4 *a = reinterpret_cast<const uint4 *>(p.a + ((size_t)id * p.rank + j0) * p.K);
+    const int chunks = p.K / 8;  // per row
+    float s[RJ] = {};
+#pragma unroll 2
+    for (int c = threadIdx.x; c < chunks; c += kInnerThreads) {
+        const uint4 xv = __ldg(x + c);
+        uint4 av[RJ];
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            s = fmaf(bf16_to_f32(xw[h] & 0xFFFFu), bf16_to_f32(aw[h] & 0xFFFFu), s);
-            s = fmaf(bf16_to_f32(xw[h] >> 16), bf16_to_f32(aw[h] >> 16), s);
+        for (int j = 0; j < RJ; ++j) av[j] = __ldg(a + (size_t)j * chunks + c);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+            const uint32_t aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                s[j] = fmaf(bf16_to_f32(xw[h] & 0xFFFFu), bf16_to_f32(aw[h] & 0xFFFFu), s[j]);
+                s[j] = fmaf(bf16_to_f32(xw[h] >> 16), bf16_to_f32(aw[h] >> 16), s[j]);
+            }
         }
     }
-    s = warp_sum(s);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kInnerThreads / 32; ++w) s += red[w];
-        p.v[(size_t)t * p.rank + j] = s * p.scale[id];
+    for (int j = 0; j < RJ; ++j) {
+        s[j] = warp_sum(s[j]);
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][j] = s[j];
     }
+    __syncthreads();
+    if (threadIdx.x < RJ) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kInnerThreads / 32; ++w) v += red[w][threadIdx.x];
+        v *= p.scale[id];
+        const size_t o = (size_t)t * p.rank + j0 + threadIdx.x;
+        if (BF16)
+            reinterpret_cast<uint16_t *>(p.v)[o] = f32_to_bf16(v);
+        else
+            p.v[o] = v;
+    }
+}
+
+template <int RJ, bool BF16>
+cudaError_t launch_inner_v(const AdapterParams &p, cudaStream_t s) {
+    static PerDeviceOnce once;
+    const cudaError_t e = per_device_once(once, [] { return smem_attributes(inner_kernel<RJ, BF16>, 0); });
+    if (e != cudaSuccess) return e;
+    return launch_ex(inner_kernel<RJ, BF16>, dim3(p.T * ((p.rank + RJ - 1) / RJ)), dim3(kInnerThreads), 0, s, true, p);
 }
 
 constexpr size_t kSmemMost = 220 * 1024;
@@ -328,12 +357,18 @@ cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s)
     return launch_gemv<true, MOE_ACT_GELU_TANH>(g, num_sms, s);
 }
 
+// v in FP32 (read by gemv_kernel) or BF16 (by the tensor-core projection).
+// rank is a multiple of 8: four rank rows per CTA, or one where those leave
+// SMs idle.
+cudaError_t launch_inner(const AdapterParams &p, bool bf16, int num_sms, cudaStream_t s) {
+    if ((int64_t)p.T * (p.rank / 4) >= num_sms)
+        return bf16 ? launch_inner_v<4, true>(p, s) : launch_inner_v<4, false>(p, s);
+    return bf16 ? launch_inner_v<1, true>(p, s) : launch_inner_v<1, false>(p, s);
+}
+
 cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s) {
     if (p.n > 0) {
-        static PerDeviceOnce once;
-        cudaError_t e = per_device_once(once, [] { return smem_attributes(inner_kernel, 0); });
-        if (e != cudaSuccess) return e;
-        e = launch_ex(inner_kernel, dim3(p.T * p.rank), dim3(kInnerThreads), 0, s, true, p);
+        const cudaError_t e = launch_inner(p, false, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     GemvArgs g = {};
