@@ -1268,12 +1268,14 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.n = p.n;
         g.rank = p.rank;
         // Few tokens: inner products by plain loads, 1.25 x 2 T rank K bytes
-        // through L2 (about 8 TB/s), and v B^T as the rows are finished, 2 x
-        // width rank bytes per row of a CTA (about 64 per clock).  Otherwise both
-        // on the tensor cores.
-        const double inner_us = 2.5 * p.T * (double)p.rank * p.K / 8e6;
+        // through L2 (about 6 TB/s) and 1.5 us for each time the SMs fill with
+        // CTAs, against about 8 us of kInner; v B^T as the rows are finished, 2 x
+        // width rank bytes per row of a CTA (16 per clock: every lane's load is
+        // a line of its own), against about 2 us of appended blocks.
+        const double inner_us = 2.5 * p.T * (double)p.rank * p.K / 6e6 +
+                                1.5 * ceil_div((int64_t)p.T * p.rank / 4, 16 * num_sms);
         const double rows = (p.T < 128 ? p.T : 128) / (double)plan.splits;
-        const double add_us = rows * plan.width * 2 * p.rank / 64 / 1900;
+        const double add_us = rows * plan.width * 2 * p.rank / 16 / 1900;
         g.direct = !plan.pairs && add_us < 2;
         if (!plan.pairs && inner_us < 8) {
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
