@@ -318,16 +318,35 @@ __device__ __forceinline__ bool append_block(const AppendRow &f, uint8_t *a, uin
     return bad;
 }
 
-// The terms that append_block left out, of row `row` with adapter id, added
-// to outputs n .. n + w - 1.
-__device__ __noinline__ void add_left_out(const GemmArgs &g, int64_t row, int n, float *v, int w) {
+// The terms that append_block left out, of row `row`, added to outputs n .. n +
+// W - 1 (v: the row's, lora_b: the adapter's from row n on).  Out of line and by value: an array whose address
+// leaves the kernel would live in local memory on the ordinary way too.
+template <int W>
+struct Sums {
+    float v[W];
+};
+template <int W>
+__device__ __noinline__ Sums<W> with_left_out(int id, const uint16_t *v, const uint16_t *lora_b, int rank,
+                                              Sums<W> s) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll 1
+        for (int j = 0; j < rank; ++j) {
+            const uint16_t b = lora_b[(size_t)i * rank + j];
+            if ((b & 0x7F80u) == 0x7F80u) s.v[i] += bf16_to_f32(v[j]) * bf16_to_f32(b);
+        }
+    return s;
+}
+template <int W>
+__device__ __forceinline__ void add_left_out(const GemmArgs &g, int64_t row, int n, float (&v)[W]) {
     const int id = g.ids[row];
     if (id < 0 || id >= g.n) return;
-    for (int i = 0; i < w; ++i)
-        for (int j = 0; j < g.rank; ++j) {
-            const uint16_t b = g.lora_b[((size_t)id * g.N + n + i) * g.rank + j];
-            if ((b & 0x7F80u) == 0x7F80u) v[i] += bf16_to_f32(g.v[row * g.rank + j]) * bf16_to_f32(b);
-        }
+    Sums<W> s;
+#pragma unroll
+    for (int i = 0; i < W; ++i) s.v[i] = v[i];
+    s = with_left_out<W>(id, g.v + row * g.rank, g.lora_b + ((size_t)id * g.N + n) * g.rank, g.rank, s);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = s.v[i];
 }
 
 // v B^T of row `row`, added to outputs n .. n + 3 (the form for few tokens: a
@@ -609,7 +628,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                             fu[i] = gated(MODE) ? __uint_as_float(u[8 * q + i]) : 0.f;
                         }
                         if (MODE == kProj && adapters && *(volatile int *)&s_ad.bad)
-                            add_left_out(g, m, n + c + 8 * q, fv, 8);
+                            add_left_out<8>(g, m, n + c + 8 * q, fv);
                         finish<MODE, ACT, 8>(g, m, half, n + c + 8 * q, fv, fu, side_words<MODE, 8>(g, m, n + c + 8 * q));
                     }
                 }
@@ -949,7 +968,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         continue;
                     }
                     if (MODE == kProj && g.direct) add_direct(g, m, n0 + col[k], v[k]);
-                    if (MODE == kProj && bad) add_left_out(g, m, n0 + col[k], v[k], 4);
+                    if (MODE == kProj && bad) add_left_out<4>(g, m, n0 + col[k], v[k]);
                     finish<MODE, ACT, 4>(g, m, half, n0 + col[k], v[k], u[k], side[k]);
                 }
             }
