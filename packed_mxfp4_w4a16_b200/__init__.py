@@ -7,21 +7,24 @@ stream gives the CUDA stream, every step of the computation runs in the
 library's kernels. There is no CPU fallback: if the library is missing or the
 device is not sm_100, the calls raise.
 
-``MoELayer`` and ``MoEStack`` bundle the calls with their buffers: a single
-layer (route + experts + combine) and a stack of layers (weightless RMSNorm,
-route, experts, combine with residual add, per layer) captured in one CUDA
+``MoELayer``, ``DenseFFN`` and ``MoEStack`` bundle the calls with their buffers:
+a single MoE layer (route + experts + combine), a dense feed-forward layer
+(gated block + down projection, with a low-rank adapter per request), and a
+stack of layers (weightless RMSNorm, route, experts, combine with residual add,
+per layer; dense layers where the model has them) captured in one CUDA
 graph per decode step.
 """
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
 from ._lib import MoEError, check, library_path, load
 
 __all__ = [
-    "MoEError", "MoELayer", "MoEStack", "library_path", "load",
+    "MoEError", "MoELayer", "DenseFFN", "MoEStack", "library_path", "load",
     "moe_create", "moe_destroy", "moe_load_packed", "moe_load_packed_nvfp4", "moe_load_packed_sym8",
     "moe_load_expert_table",
     "moe_workspace_bytes", "moe_set_workspace", "moe_route", "moe_route_ex",
@@ -358,34 +361,33 @@ def moe_stack_set_spin_limit(s: int, polls: int) -> None:
 
 
 # ------------------------------------------- dense feed-forward layers
+# A call at small sizes is a few microseconds on the GPU, so the checks below
+# are written to cost little: plain conditions first, the names of what failed
+# only on the way to the error.
 
-def _shaped(t, dtype, shape, name, what):
-    """t is a contiguous CUDA tensor of this dtype and shape, else MoEError
-    (the C calls take bare pointers and cannot check sizes)."""
-    if t is None or not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise MoEError(f"{name} ({what})", -1)
+_BF16 = torch.bfloat16
 
 
-def _raw_stream(stream, like):
-    """cudaStream_t of `stream`, or of the current stream of the device of
-    `like` (the C calls refuse memory of any but the current device)."""
+def _is(t, dtype, shape):
+    """t is a contiguous tensor of this dtype and shape (the C calls take bare
+    pointers and cannot check sizes; they refuse host memory and other
+    devices)."""
+    return t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
+def _expect(name, **wants):
+    """Raise MoEError naming the first of what=(tensor, dtype, shape) that is
+    not as wanted."""
+    for what, (t, dtype, shape) in wants.items():
+        if not _is(t, dtype, shape):
+            raise MoEError(f"{name} ({what})", -1)
+
+
+def _new(like, shape, stream):
+    """A new BF16 output beside `like`, used on `stream`."""
+    t = torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
     if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(like.get_device())
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _out(t, like, shape, name, what, stream):
-    """The caller's output tensor, checked, or a new one beside `like`."""
-    if t is None:
-        t = like.new_empty(shape)
-        if stream is not None:
-            t.record_stream(stream)
-    else:
-        _shaped(t, torch.bfloat16, shape, name, what)
+        t.record_stream(stream)
     return t
 
 
@@ -394,18 +396,32 @@ def _workspace(ws, need, like, name, stream):
         ws = like.new_empty(need, dtype=torch.uint8)
         if stream is not None:
             ws.record_stream(stream)
-    elif not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise MoEError(f"{name} (workspace)", -1)
     return ws
+
+
+def _raw_stream(stream, like):
+    """cudaStream_t of `stream`, or of the current stream of the device of
+    `like` (the C calls refuse memory of any but the current device)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if not like.is_cuda:
+        return None
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _gated_shapes(x, w_gate, w_up, name):
     if x is None or x.dim() != 2 or w_gate is None or w_gate.dim() != 2:
         raise MoEError(f"{name} (shape)", -1)
     (T, H), I = x.shape, w_gate.shape[0]
-    _shaped(x, torch.bfloat16, (T, H), name, "x")
-    _shaped(w_gate, torch.bfloat16, (I, H), name, "w_gate")
-    _shaped(w_up, torch.bfloat16, (I, H), name, "w_up")
+    wshape = (I, H)
+    if not (_is(x, _BF16, (T, H)) and _is(w_gate, _BF16, wshape) and _is(w_up, _BF16, wshape)):
+        _expect(name, x=(x, _BF16, (T, H)), w_gate=(w_gate, _BF16, wshape), w_up=(w_up, _BF16, wshape))
     return T, H, I
 
 
@@ -415,14 +431,19 @@ def moe_gated_ffn(x, w_gate, w_up, act=ACT_SILU, h=None, flags=0, x_norm=None, s
     FFN_RMSNORM x is a residual stream and x_norm [T, H] receives the
     normalised input."""
     T, H, I = _gated_shapes(x, w_gate, w_up, "moe_gated_ffn")
-    h = _out(h, x, (T, I), "moe_gated_ffn", "h", stream)
-    if x_norm is not None:
-        _shaped(x_norm, torch.bfloat16, (T, H), "moe_gated_ffn", "x_norm")
+    if h is None:
+        h = _new(x, (T, I), stream)
+    elif not _is(h, _BF16, (T, I)):
+        raise MoEError("moe_gated_ffn (h)", -1)
+    if x_norm is not None and not _is(x_norm, _BF16, (T, H)):
+        raise MoEError("moe_gated_ffn (x_norm)", -1)
     check("moe_gated_ffn", load().moe_gated_ffn(
-        _ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), act, flags, _ptr(x_norm), _ptr(h), _raw_stream(stream, x)))
+        x.data_ptr(), T, H, I, w_gate.data_ptr(), w_up.data_ptr(), act, flags, _ptr(x_norm),
+        h.data_ptr(), _raw_stream(stream, x)))
     return h
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_gated_ffn_backward_workspace_bytes(T: int, H: int, I: int) -> int:
     n = C.c_size_t()
     check("moe_gated_ffn_backward_workspace_bytes",
@@ -437,22 +458,30 @@ def moe_gated_ffn_backward(x, w_gate, w_up, dh, act=ACT_SILU, dx=None, dw_gate=N
     Outputs and workspace (uint8) that are not given are new tensors."""
     name = "moe_gated_ffn_backward"
     T, H, I = _gated_shapes(x, w_gate, w_up, name)
-    _shaped(dh, torch.bfloat16, (T, I), name, "dh")
+    if not _is(dh, _BF16, (T, I)):
+        raise MoEError(f"{name} (dh)", -1)
     if (not need_dx and dx is not None) or (not need_dw and (dw_gate is not None or dw_up is not None)):
         raise MoEError(f"{name} (an output that is not needed)", -1)
     if need_dx:
-        dx = _out(dx, x, (T, H), name, "dx", stream)
+        if dx is None:
+            dx = _new(x, (T, H), stream)
+        elif not _is(dx, _BF16, (T, H)):
+            raise MoEError(f"{name} (dx)", -1)
     if need_dw:
-        dw_gate = _out(dw_gate, x, (I, H), name, "dw_gate", stream)
-        dw_up = _out(dw_up, x, (I, H), name, "dw_up", stream)
+        if dw_gate is None:
+            dw_gate = _new(w_gate, (I, H), stream)
+        if dw_up is None:
+            dw_up = _new(w_up, (I, H), stream)
+        _expect(name, dw_gate=(dw_gate, _BF16, (I, H)), dw_up=(dw_up, _BF16, (I, H)))
     workspace = _workspace(workspace, moe_gated_ffn_backward_workspace_bytes(T, H, I), x, name,
                            stream)
     check(name, load().moe_gated_ffn_backward(
-        _ptr(x), T, H, I, _ptr(w_gate), _ptr(w_up), act, _ptr(dh), _ptr(dx), _ptr(dw_gate), _ptr(dw_up),
-        _ptr(workspace), workspace.numel(), _raw_stream(stream, x)))
+        x.data_ptr(), T, H, I, w_gate.data_ptr(), w_up.data_ptr(), act, dh.data_ptr(), _ptr(dx),
+        _ptr(dw_gate), _ptr(dw_up), workspace.data_ptr(), workspace.numel(), _raw_stream(stream, x)))
     return dx, dw_gate, dw_up
 
 
+@functools.lru_cache(maxsize=4096)
 def moe_adapter_proj_workspace_bytes(T: int, K: int, N: int, n_adapters: int, rank: int) -> int:
     n = C.c_size_t()
     check("moe_adapter_proj_workspace_bytes",
@@ -471,32 +500,35 @@ def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_id
     if x is None or x.dim() != 2 or w is None or w.dim() != 2:
         raise MoEError(f"{name} (shape)", -1)
     (T, K), N = x.shape, w.shape[0]
-    _shaped(x, torch.bfloat16, (T, K), name, "x")
-    _shaped(w, torch.bfloat16, (N, K), name, "w")
-    n = rank = 0
-    given = [t is not None for t in (lora_a, lora_b, lora_scale, adapter_ids)]
-    if any(given):
-        if not all(given) or lora_a.dim() != 3:
+    if not (_is(x, _BF16, (T, K)) and _is(w, _BF16, (N, K))):
+        _expect(name, x=(x, _BF16, (T, K)), w=(w, _BF16, (N, K)))
+    n = rank = need = 0
+    pa = pb = ps = pi = pw = None
+    if lora_a is not None:
+        if lora_a.dim() != 3 or lora_a.shape[0] == 0:
             raise MoEError(f"{name} (adapters)", -1)
-        n, rank = lora_a.shape[:2]
-        if n == 0:
-            raise MoEError(f"{name} (adapters)", -1)
-        _shaped(lora_a, torch.bfloat16, (n, rank, K), name, "lora_a")
-        _shaped(lora_b, torch.bfloat16, (n, N, rank), name, "lora_b")
-        _shaped(lora_scale, torch.float32, (n,), name, "lora_scale")
-        _shaped(adapter_ids, torch.int32, (T,), name, "adapter_ids")
-    if residual is not None:
-        _shaped(residual, torch.bfloat16, (T, N), name, "residual")
-    y = _out(y, x, (T, N), name, "y", stream)
-    need = moe_adapter_proj_workspace_bytes(T, K, N, n, rank)
-    if need:
-        workspace = _workspace(workspace, need, x, name, stream)
-    else:
-        workspace = None
+        n, rank, _ = lora_a.shape
+        if not (_is(lora_a, _BF16, (n, rank, K)) and _is(lora_b, _BF16, (n, N, rank))
+                and _is(lora_scale, torch.float32, (n,)) and _is(adapter_ids, torch.int32, (T,))):
+            _expect(name, lora_a=(lora_a, _BF16, (n, rank, K)), lora_b=(lora_b, _BF16, (n, N, rank)),
+                    lora_scale=(lora_scale, torch.float32, (n,)),
+                    adapter_ids=(adapter_ids, torch.int32, (T,)))
+        pa, pb, ps, pi = (lora_a.data_ptr(), lora_b.data_ptr(), lora_scale.data_ptr(),
+                          adapter_ids.data_ptr())
+        workspace = _workspace(workspace, moe_adapter_proj_workspace_bytes(T, K, N, n, rank), x,
+                               name, stream)
+        need, pw = workspace.numel(), workspace.data_ptr()
+    elif lora_b is not None or lora_scale is not None or adapter_ids is not None:
+        raise MoEError(f"{name} (adapters)", -1)
+    if residual is not None and not _is(residual, _BF16, (T, N)):
+        raise MoEError(f"{name} (residual)", -1)
+    if y is None:
+        y = _new(x if residual is None else residual, (T, N), stream)
+    elif not _is(y, _BF16, (T, N)):
+        raise MoEError(f"{name} (y)", -1)
     check(name, load().moe_adapter_proj(
-        _ptr(x), T, K, N, _ptr(w), _ptr(residual), n, rank, _ptr(lora_a), _ptr(lora_b), _ptr(lora_scale),
-        _ptr(adapter_ids), _ptr(y), _ptr(workspace), workspace.numel() if workspace is not None else 0,
-        _raw_stream(stream, x)))
+        x.data_ptr(), T, K, N, w.data_ptr(), _ptr(residual), n, rank, pa, pb, ps, pi, y.data_ptr(),
+        pw, need, _raw_stream(stream, x)))
     return y
 
 
@@ -597,18 +629,77 @@ class MoELayer:
         return moe_get_status(self.handle)
 
 
+class DenseFFN:
+    """A dense feed-forward layer bound to BF16 weights already on the device:
+    h = act(x w_gate^T) * (x w_up^T), y = h w_down^T (+ the adapter of each
+    token's request) (+ residual).  w_gate, w_up [I, H], w_down [H, I];
+    ``lora``: None or (lora_a BF16 [n, rank, I], lora_b BF16 [n, H, rank],
+    lora_scale FP32 [n]), adapters of the down projection.
+
+    The layer keeps the buffers of up to ``max_tokens`` tokens (h, the
+    normalised input, the adapters' workspace), so its calls must be ordered
+    on the GPU; captured in a CUDA graph they stay valid as long as the layer."""
+
+    def __init__(self, w_gate, w_up, w_down, act=ACT_SILU, lora=None, max_tokens=4):
+        moe_device_check()
+        _gated_shapes(w_gate, w_gate, w_up, "DenseFFN")
+        self.I, self.H = w_gate.shape
+        _expect("DenseFFN", w_down=(w_down, _BF16, (self.H, self.I)))
+        self.w_gate, self.w_up, self.w_down, self.act, self.lora = w_gate, w_up, w_down, act, lora
+        self.max_tokens = max_tokens
+        self.h = w_gate.new_empty(max_tokens, self.I)
+        self.x_norm = w_gate.new_empty(max_tokens, self.H)
+        need = 0
+        if lora is not None:
+            n, rank = lora[0].shape[:2]
+            need = max(moe_adapter_proj_workspace_bytes(t, self.I, self.H, n, rank)
+                       for t in {max_tokens, min(max_tokens, 8)})
+        self.workspace = w_gate.new_empty(need, dtype=torch.uint8)
+
+    def forward(self, x, adapter_ids=None, residual=None, y=None, rmsnorm=False, stream=None):
+        """y [T, H] for x [T, H], T <= max_tokens.  rmsnorm: x is a residual
+        stream, the layer runs on its RMSNorm.  adapter_ids int32 [T] (-1:
+        none); None: no adapters.  residual may be y."""
+        T = x.shape[0]
+        if T > self.max_tokens:
+            raise MoEError("DenseFFN.forward", -5)
+        moe_gated_ffn(x, self.w_gate, self.w_up, self.act, self.h[:T],
+                      FFN_RMSNORM if rmsnorm else 0, self.x_norm[:T] if rmsnorm else None, stream)
+        if self.lora is None or adapter_ids is None:
+            return moe_adapter_proj(self.h[:T], self.w_down, residual=residual, y=y, stream=stream)
+        return moe_adapter_proj(self.h[:T], self.w_down, *self.lora, adapter_ids, residual=residual,
+                                y=y, workspace=self.workspace, stream=stream)
+
+    def __call__(self, x, adapter_ids=None, stream=None):
+        return self.forward(x, adapter_ids, stream=stream)
+
+    def gated_backward(self, x, dh, stream=None):
+        """(dx, dw_gate, dw_up) of the gated block for dh = dL/dh [T, I] (any
+        T; a workspace of its own per call)."""
+        return moe_gated_ffn_backward(x, self.w_gate, self.w_up, dh, self.act, stream=stream)
+
+    def status(self, stream=None) -> int:
+        """Status bits of the dense calls on the current device (cleared)."""
+        return moe_dense_status(stream)
+
+    def close(self):
+        pass
+
+
 class MoEStack:
     """A stack of MoE layers run as one decode step on a residual stream r:
     per layer xn = RMSNorm(r) (weightless, eps 1e-6), route(xn), experts,
     r = BF16(r + combine).  ``step()`` replays one CUDA graph of all layers.
     Layers share one workspace (they run in order on one stream).
     ``layers_weights``: per layer (codes, scales, router_w, router_b), or
-    with a fifth item, the NVFP4 multipliers [E, 2] (see MoELayer).
+    with a fifth item, the NVFP4 multipliers [E, 2] (see MoELayer); or a
+    DenseFFN of the same H and max_tokens >= T: r = BF16(r + FFN(RMSNorm(r))),
+    with the adapters that ``adapter_ids`` (int32 [T], -1 at first) names.
 
-    ``persistent``: run the whole step as one launch (moe_stack_decode);
+    ``persistent``: run all MoE layers as one launch (moe_stack_decode);
     None = when the shape allows it (T = 1, MXFP4 layers, shapes of
-    moe_stack_create), False = one layer at a time (moe_layer_ex), True =
-    required."""
+    moe_stack_create, dense layers only ahead of the MoE layers), False = one
+    layer at a time (moe_layer_ex), True = required."""
 
     def __init__(self, layers_weights, E, H, I, top_k, T=1, device="cuda", persistent=None):
         moe_device_check()
@@ -616,6 +707,11 @@ class MoEStack:
         self.layers = []
         ws = None
         for lw in layers_weights:
+            if isinstance(lw, DenseFFN):
+                if lw.H != H or lw.max_tokens < T:
+                    raise MoEError("MoEStack (dense layer)", -1)
+                self.layers.append(lw)
+                continue
             codes, scales, router_w, router_b = lw[:4]
             gscales = lw[4] if len(lw) > 4 else None
             L = MoELayer(E, H, I, top_k, codes, scales, router_w, router_b, max_tokens=T,
@@ -624,6 +720,11 @@ class MoEStack:
             self.layers.append(L)
         dev = torch.device(device)
         n = len(self.layers)
+        self.moe_layers = [L for L in self.layers if isinstance(L, MoELayer)]
+        # dense layers ahead of all MoE layers, and whether there are others
+        self.lead = next((l for l, L in enumerate(self.layers) if isinstance(L, MoELayer)), n)
+        mixed = self.lead + len(self.moe_layers) != n
+        self.adapter_ids = torch.full((T,), -1, dtype=torch.int32, device=dev)
         self.r = torch.zeros(T, H, dtype=torch.bfloat16, device=dev)
         self.xn = torch.zeros(T, H, dtype=torch.bfloat16, device=dev)
         self.ids = torch.zeros(n, T, top_k, dtype=torch.int32, device=dev)
@@ -633,11 +734,11 @@ class MoEStack:
         # one launch for the whole step (moe_stack_*) when the shape allows it
         self.stack = None
         self.stack_ws = None
-        if persistent is not False and T == 1:
+        if persistent is not False and T == 1 and self.moe_layers and not mixed:
             try:
-                self.stack = moe_stack_create([L.handle for L in self.layers],
-                                              [L.router_w for L in self.layers],
-                                              [L.router_b for L in self.layers])
+                self.stack = moe_stack_create([L.handle for L in self.moe_layers],
+                                              [L.router_w for L in self.moe_layers],
+                                              [L.router_b for L in self.moe_layers])
                 self.stack_ws = torch.empty(moe_stack_workspace_bytes(self.stack),
                                             dtype=torch.uint8, device=dev)
                 moe_stack_set_workspace(self.stack, self.stack_ws)
@@ -651,35 +752,46 @@ class MoEStack:
             raise MoEError("moe_stack_create", -1)
 
     def set_tuning(self, use_pdl=True, prefetch_down=True):
-        for L in self.layers:
+        for L in self.moe_layers:
             moe_set_tuning(L.handle, use_pdl, prefetch_down)
 
     def set_fusion(self, mode):
         """Launch structure of every layer (FUSION_NONE / _ROUTER / _LAYER)."""
-        for L in self.layers:
+        for L in self.moe_layers:
             moe_set_fusion(L.handle, mode)
 
     def enqueue(self, stream=None):
         """Enqueue one decode step (all layers) on `stream`."""
         if self.stack is not None:
-            moe_stack_decode(self.stack, self.r, topk_ids=self.ids, topk_w=self.w, stream=stream)
+            for L in self.layers[:self.lead]:
+                self._enqueue_dense(L, stream)
+            moe_stack_decode(self.stack, self.r, topk_ids=self.ids[self.lead:],
+                             topk_w=self.w[self.lead:], stream=stream)
         else:
             self.enqueue_layers(stream)
 
+    def _enqueue_dense(self, L, stream):
+        L.forward(self.r, self.adapter_ids, residual=self.r, y=self.r, rmsnorm=True, stream=stream)
+
     def enqueue_layers(self, stream=None):
-        """The same step as one moe_layer_ex call per layer."""
+        """The same step as one moe_layer_ex call per MoE layer."""
         for l, L in enumerate(self.layers):
+            if isinstance(L, DenseFFN):
+                self._enqueue_dense(L, stream)
+                continue
             moe_layer_ex(L.handle, self.r, L.router_w, L.router_b, ROUTE_RMSNORM, self.xn, None,
                          self.ids[l], self.w[l], self.r, self.r, 0, stream)
 
     def status(self, stream=None) -> int:
-        """Device status bits of the stack kernel and of every layer handle
-        (synchronises), cleared."""
+        """Device status bits of the stack kernel, of every layer handle and,
+        with dense layers, of the dense calls (synchronises), cleared."""
         st = 0
         if self.stack is not None:
             st |= moe_stack_get_status(self.stack, stream)
-        for L in self.layers:
+        for L in self.moe_layers:
             st |= L.status()
+        if len(self.moe_layers) != len(self.layers):
+            st |= moe_dense_status(stream)
         return st
 
     def capture(self):
