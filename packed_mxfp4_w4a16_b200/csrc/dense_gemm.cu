@@ -53,23 +53,23 @@ constexpr bool gated(int mode) { return mode == kFwd || mode == kBwd; }
 constexpr bool a_mn(int mode) { return mode == kDw; }
 constexpr bool b_mn(int mode) { return mode == kDx || mode == kDw; }
 
-// One K block of operand A: 64-row boxes of the CTA's rows from `m` on.
+// One K block of operand A from row `m` on: K-major in one box of all its
+// lines, MN-major in `boxes` boxes of 64 rows.
 template <int MODE, int CG>
 __device__ __forceinline__ void load_a(uint32_t dst, const CUtensorMap *a, const GemmArgs &g, int kb, int m,
                                        int half, int boxes, uint32_t bar) {
-    for (int i = 0; i < boxes; ++i) {
-        if (MODE == kDx) {
-            const int h = kb >= g.kb_half;
-            tc::load3<CG>(dst + i * tc::kBox, a, (kb - h * g.kb_half) * 64, h, m + 64 * i, bar);
-        } else if (MODE == kDw) {
-            tc::load3<CG>(dst + i * tc::kBox, a, m + 64 * i, half, kb * 64, bar);
-        } else {
-            tc::load2<CG>(dst + i * tc::kBox, a, kb * 64, m + 64 * i, bar);
-        }
+    if (MODE == kDx) {
+        const int h = kb >= g.kb_half;
+        tc::load3<CG>(dst, a, (kb - h * g.kb_half) * 64, h, m, bar);
+    } else if (MODE == kDw) {
+        for (int i = 0; i < boxes; ++i) tc::load3<CG>(dst + i * tc::kBox, a, m + 64 * i, half, kb * 64, bar);
+    } else {
+        tc::load2<CG>(dst, a, kb * 64, m, bar);
     }
 }
 
-// One box (64 columns of the output, or 64 rows of Wg / Wu) of operand B.
+// One box (MN-major: 64 columns of the output; K-major: the map's lines of a
+// weight) of operand B.
 template <int MODE, int CG>
 __device__ __forceinline__ void load_b(uint32_t dst, const CUtensorMap *b0, const CUtensorMap *b1,
                                        const GemmArgs &g, int kb, int n, int second, uint32_t bar) {
@@ -377,10 +377,11 @@ __device__ __forceinline__ void add_direct(const GemmArgs &g, int64_t row, int n
 }
 
 // ------------------------------------------------------- large products --
-// A pair of CTAs (cluster of 2, cta_group::2) owns 256 x 256 accumulators:
+// A pair of CTAs (cluster of 2, cta_group::2) owns 256 x `cols` accumulators
+// (cols up to 256, fewer where that leaves fewer SMs without a tile at the end):
 // each CTA loads and keeps its 128 rows of A and half of B's rows, the
 // leader's MMAs read both CTAs' shared memory, and each CTA's TMEM receives
-// its 128 rows.  Gated: one CTA brings 128 rows of Wg, the other 128 of Wu,
+// its 128 rows.  Gated: one CTA brings cols / 2 rows of Wg, the other as many of Wu,
 // so a row's g and u meet in one thread.  Persistent: pairs walk the tiles
 // with a stride of the pair count; two accumulators of 256 columns, so the
 // epilogue of one tile runs under the products of the next.
@@ -412,6 +413,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     const uint32_t rank = tc::cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const int tiles = g.mt * g.nt;
+    const int half_cols = g.cols / 2;  // lines of B in each CTA
+    const uint32_t bytes = 2 * tc::kBox + half_cols * 128;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBigStages; ++i) {
@@ -457,7 +460,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         half = MODE == kDw && mt >= g.mt_half;
         if (half) mt -= g.mt_half;
         m = mt * 256;
-        n = nt * (gated(MODE) ? 128 : 256);
+        n = nt * g.width;
     };
 
     if (warp == 0) {
@@ -470,7 +473,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             int m, half, n;
             place(t, m, half, n);
             m += rank * 128;
-            if (!gated(MODE)) n += rank * 128;
+            if (!gated(MODE)) n += rank * half_cols;
 #pragma unroll 1
             for (int kb = 0; kb < g.kb; ++kb, at.next(kBigStages)) {
                 if (at.pass > 0) {
@@ -480,11 +483,11 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 }
                 if (issue) {
                     const uint32_t bar = bar0 + 8 * at.slot, dst = smem + at.slot * kBigStage;
-                    tc::arrive_tx_cluster(bar, kBigStage);
+                    tc::arrive_tx_cluster(bar, bytes);
                     load_a<MODE, 2>(dst, &map_a, g, kb, m, half, 2, bar);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        load_b<MODE, 2>(dst + (2 + i) * tc::kBox, &map_b0, &map_b1, g, kb, n + 64 * i, rank, bar);
+                    load_b<MODE, 2>(dst + 2 * tc::kBox, &map_b0, &map_b1, g, kb, n, rank, bar);
+                    if (b_mn(MODE) && half_cols > 64)
+                        load_b<MODE, 2>(dst + 3 * tc::kBox, &map_b0, &map_b1, g, kb, n + 64, rank, bar);
                 }
                 __syncwarp();
             }
@@ -497,7 +500,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            constexpr uint32_t id = tc::idesc(256, 256, a_mn(MODE), b_mn(MODE));
+            const uint32_t id = tc::idesc(256, g.cols, a_mn(MODE), b_mn(MODE));
             const uint64_t a0 = tc::desc<a_mn(MODE)>(smem), b0 = tc::desc<b_mn(MODE)>(smem + 2 * tc::kBox);
             const bool issue = tc::elect();
             tc::Ring at;
@@ -572,14 +575,14 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 const int blocks = adapter_blocks(s_ad.count, g.rank);
                 AppendRow f;
                 if (blocks)
-                    fetch_block(f, s_ad, g, 0, m + rank * 128, rank * 128, n + rank * 128, 128, tid, true);
+                    fetch_block(f, s_ad, g, 0, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid, true);
 #pragma unroll 1
                 for (int e = 0; e < (blocks ? blocks : 1); ++e, ++x) {
                     if (x > 0) {
                         ok = group_all(tc::wait(&s_xempty, (x - 1) & 1, abort));  // the whole group goes on or leaves
                         if (!ok) break;
                     }
-                    if (blocks && append_block(f, xa, xb, 128, 128, tid)) {
+                    if (blocks && append_block(f, xa, xb, 128, half_cols, tid)) {
                         s_ad.bad = 1;
                         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
                     }
@@ -588,7 +591,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     group_sync();
                     if (tid == 0) tc::arrive_release_cluster(xfull);
                     if (e + 1 < blocks)
-                        fetch_block(f, s_ad, g, e + 1, m + rank * 128, rank * 128, n + rank * 128, 128, tid, false);
+                        fetch_block(f, s_ad, g, e + 1, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid, false);
                 }
                 group_sync();  // the list is rebuilt for the next tile
             }
@@ -608,14 +611,12 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             place(t, m, half, n);
             m += rank * 128 + (warp & 3) * 32 + lane;
             const uint32_t acc = base + buf * 256;
-            // gated: two warps share the rows, each finishes half of the columns
-            const int c0 = gated(MODE) && warp >= 8 ? 64 : 0;
-            const int c1 = gated(MODE) ? c0 + 64 : 256;
+            // gated: two warps share the rows, each finishes every other 16 columns
 #pragma unroll 1
-            for (int c = c0; c < c1 && n + c < g.N; c += 16) {
+            for (int c = gated(MODE) && warp >= 8 ? 16 : 0; c < g.width && n + c < g.N; c += gated(MODE) ? 32 : 16) {
                 uint32_t v[16], u[16];
                 tc::tmem_ld16(acc + c, v);
-                if (gated(MODE)) tc::tmem_ld16(acc + 128 + c, u);
+                if (gated(MODE)) tc::tmem_ld16(acc + half_cols + c, u);
                 tc::tmem_wait();
                 if (m < g.M) {
 #pragma unroll
@@ -747,10 +748,9 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int a0 = MODE == kInner ? w / g.parts * g.per_tile : 0;
         const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
         if (warp == 0) {
-            // boxes that hold rows; what the products read beyond is garbage that
-            // stays in its rows
-            const int full = rows > 64 ? 2 : 1;
-            const uint32_t bytes = full * min(a_lines, 64) * 128 + (MODE == kInner  ? slots * lines * 128
+            // (rows that the products read beyond a_lines are garbage that stays in
+            // its rows)
+            const uint32_t bytes = a_lines * 128 + (MODE == kInner  ? slots * lines * 128
                                                                     : gated(MODE) ? 2 * g.width * 128
                                                                                   : g.width * 128);
             const bool issue = tc::elect();
@@ -778,7 +778,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         if (b_mn(MODE) && g.width > 64)
                             load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb, n0 + 64, 0, bar);
                     }
-                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, full, bar);
+                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, a_lines / 64, bar);
                 }
                 __syncwarp();
             }
@@ -1021,9 +1021,11 @@ struct Maps {
 constexpr int kMaxSplits = 8;  // portable cluster size
 constexpr size_t kSmallSmem = 200 * 1024;  // of one CTA's stages
 
-// Lines of A in a stage of the single-CTA kernel: the rows there are (8-line
-// groups of the swizzle), 128 for more than 64.
-int a_lines(int mode, int M) { return M > 64 ? 128 : a_mn(mode) ? 64 : (M + 7) / 8 * 8; }
+// Lines of A in a CTA's stage: 128; in the single-CTA kernel the rows there are
+// (8-line groups of the swizzle) where they are 64 or fewer.
+int a_lines(int mode, int M, bool pairs = false) {
+    return pairs || M > 64 ? 128 : a_mn(mode) ? 64 : (M + 7) / 8 * 8;
+}
 
 // How many clusters of 2, 4 and 8 CTAs that fill an SM each can run at the
 // same time on the current device (GPCs have SMs that no cluster can use).
@@ -1044,12 +1046,12 @@ struct Plan {
 // the operands come from L2 (a pair's products keep up with that, 0.28 us per
 // block), about 45 where every byte comes from HBM; the share between is the
 // matrices' bytes over all that is loaded.  However few its bytes, a block
-// takes 0.25 us of issue and waits.
+// takes 0.2 us of issue and waits.
 double stream_us(int64_t ctas, int blocks, double stage, double once, int num_sms) {
     const double all = stage * blocks * (double)ctas, share = once < all ? once / all : 1.0;
     const double waves = (double)((ctas + num_sms - 1) / num_sms);
     const double block = stage * 1e-3 * (share / 45 + (1 - share) / 117);
-    return waves * blocks * (block > 0.25 ? block : 0.25);
+    return waves * blocks * (block > 0.2 ? block : 0.2);
 }
 
 // Pairs of CTAs with 256-row tiles, or single ones with a tile width and a
@@ -1058,9 +1060,14 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
     const int halves = mode == kDw ? 2 : 1, most = gated(mode) ? 64 : 128;
     const double once = 128.0 * g.kb * ((double)g.M * halves + (double)g.N * (gated(mode) ? 2 : 1));
     Plan best = {1e30, true, 1, 0, 0, 0};
-    if (g.M > 128) {
-        const int64_t tiles = (int64_t)ceil_div(g.M, 256) * halves * ceil_div(g.N, 2 * most);
-        best.us = stream_us(2 * tiles, g.kb, 4.0 * tc::kBox, once, num_sms / 2 * 2);
+    // narrower pair tiles only where every wave is full of work: a block's
+    // products and its loads shrink with the columns, its rows of A do not
+    for (int cols = 256; g.M > 128 && cols >= 128; cols -= b_mn(mode) ? 128 : 32) {
+        Plan p = {0, true, 1, gated(mode) ? cols / 2 : cols, cols, 0};
+        p.nt = ceil_div(g.N, p.width);
+        const int64_t tiles = (int64_t)ceil_div(g.M, 256) * halves * p.nt;
+        p.us = stream_us(2 * tiles, g.kb, 2.0 * tc::kBox + cols * 64, once, num_sms / 2 * 2);
+        if (p.us < 0.97 * best.us) best = p;
     }
     const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
     // joining the parts of a split K: about 2 us, more for larger clusters
@@ -1159,7 +1166,7 @@ cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sm
 }
 
 template <int MODE, int ACT>
-cudaError_t launch_big(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
+cudaError_t launch_big(const Maps &m, GemmArgs g, const Plan &plan, int num_sms, cudaStream_t s) {
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, [] {
         return smem_attributes(big_kernel<MODE, ACT>, kBigSmem);
@@ -1167,7 +1174,9 @@ cudaError_t launch_big(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     g.mt_half = ceil_div(g.M, 256);
     g.mt = g.mt_half * (MODE == kDw ? 2 : 1);
-    g.nt = ceil_div(g.N, gated(MODE) ? 128 : 256);
+    g.nt = plan.nt;
+    g.width = plan.width;
+    g.cols = plan.cols;
     g.n_fast = g.nt < g.mt;
     const int64_t tiles = (int64_t)g.mt * g.nt;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
@@ -1175,19 +1184,18 @@ cudaError_t launch_big(const Maps &m, GemmArgs g, int num_sms, cudaStream_t s) {
 }
 
 // Activations [rows][cols] as K-major operand A.
-cudaError_t map_tokens(CUtensorMap *m, const uint16_t *x, int64_t rows, int64_t cols) {
-    const int lines = a_lines(kFwd, (int)rows);
-    return tc::map_matrix(m, x, rows, cols, lines < 64 ? lines : 64);
+cudaError_t map_tokens(CUtensorMap *m, const uint16_t *x, int64_t rows, int64_t cols, bool pairs) {
+    return tc::map_matrix(m, x, rows, cols, a_lines(kFwd, (int)rows, pairs));
 }
 
 // A weight [rows][cols] as K-major operand B: lines per box as the plan's kernel loads them.
 cudaError_t map_weight(CUtensorMap *m, const uint16_t *w, int64_t rows, int64_t cols, const Plan &plan) {
-    return tc::map_matrix(m, w, rows, cols, plan.pairs ? 64 : plan.width);
+    return tc::map_matrix(m, w, rows, cols, plan.pairs ? plan.cols / 2 : plan.width);
 }
 
 template <int MODE, int ACT>
 cudaError_t launch_gemm(const Maps &m, const GemmArgs &g, const Plan &plan, int num_sms, cudaStream_t s) {
-    if (plan.pairs) return launch_big<MODE, ACT>(m, g, num_sms, s);
+    if (plan.pairs) return launch_big<MODE, ACT>(m, g, plan, num_sms, s);
     return launch_small<MODE, ACT>(m, g, plan, num_sms, MODE == kProj && g.n > 0, s);
 }
 
@@ -1211,7 +1219,7 @@ cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb = ceil_div(p.H, 64);
     const Plan plan = make_plan(kFwd, g, num_sms, fill);
     Maps m;
-    e = map_tokens(&m.a, p.x, p.T, p.H);
+    e = map_tokens(&m.a, p.x, p.T, p.H, plan.pairs);
     if (e == cudaSuccess) e = map_weight(&m.b0, p.wg, p.I, p.H, plan);
     if (e == cudaSuccess) e = map_weight(&m.b1, p.wu, p.I, p.H, plan);
     if (e != cudaSuccess) return e;
@@ -1228,12 +1236,6 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     ClusterFill fill;
     cudaError_t e = cluster_fill(num_sms, &fill);
     if (e != cudaSuccess) return e;
-    Maps m;
-    const int lines = a_lines(kDx, p.T);
-    e = tc::map_halves(&m.a, p.dgu, p.T, p.I, lines < 64 ? lines : 64);
-    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
-    if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
-    if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
     g.M = p.T;
@@ -1241,7 +1243,13 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     g.kb_half = ceil_div(p.I, 64);
     g.kb = 2 * g.kb_half;
     g.out0 = p.dx;
-    return launch_gemm<kDx, 0>(m, g, make_plan(kDx, g, num_sms, fill), num_sms, s);
+    const Plan plan = make_plan(kDx, g, num_sms, fill);
+    Maps m;
+    e = tc::map_halves(&m.a, p.dgu, p.T, p.I, a_lines(kDx, p.T, plan.pairs));
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b0, p.wg, p.I, p.H);
+    if (e == cudaSuccess) e = tc::map_matrix(&m.b1, p.wu, p.I, p.H);
+    if (e != cudaSuccess) return e;
+    return launch_gemm<kDx, 0>(m, g, plan, num_sms, s);
 }
 
 cudaError_t launch_dw_tc(const GatedParams &p, bool after_dx, int num_sms, cudaStream_t s) {
@@ -1268,9 +1276,6 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     ClusterFill fill;
     cudaError_t e = cluster_fill(num_sms, &fill);
     if (e != cudaSuccess) return e;
-    Maps m;
-    e = map_tokens(&m.a, p.x, p.T, p.K);
-    if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
     g.M = p.T;
@@ -1279,6 +1284,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     // (the same plan with and without adapters: a token without one gets the
     // plain projection's bits)
     const Plan plan = make_plan(kProj, g, num_sms, fill);
+    Maps m;
     if (p.n > 0) {
         g.ids = p.ids;
         g.scale = p.scale;
@@ -1300,6 +1306,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
         } else {
             const int lines = p.rank < 128 ? p.rank : 128;
+            if ((e = map_tokens(&m.a, p.x, p.T, p.K, false)) != cudaSuccess) return e;
             if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
             m.b1 = m.b0;
             g.per_tile = 128 / lines;
@@ -1322,6 +1329,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
             if (e != cudaSuccess) return e;
         }
     }
+    if ((e = map_tokens(&m.a, p.x, p.T, p.K, plan.pairs)) != cudaSuccess) return e;
     if ((e = map_weight(&m.b0, p.w, p.N, p.K, plan)) != cudaSuccess) return e;
     m.b1 = m.b0;
     g.residual = p.residual;
