@@ -664,9 +664,11 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 // memory, and each then finishes its share of the rows, adding the S parts in
 // rank order through distributed shared memory (the same bits every time, and
 // no workspace or counter that two calls could share).
-// A stage holds `lines` (8 to 128) lines of 128 bytes of A and `cols` of B: the
-// fewer the tokens, the more stages of weights are in flight.
-constexpr int kSmallMaxStages = 16;
+// A K block takes `lines` (8 to 128) lines of 128 bytes of A and `cols` of B: the
+// fewer the tokens, the more of the weights is in flight.  A stage holds two
+// blocks where there is room for three such stages: a wait, a commit and the loop around them cost the issuing warp about
+// 390 clocks, the four MMAs of a block 78.
+constexpr int kSmallMaxStages = 8;
 __host__ __device__ constexpr uint32_t small_stage(int lines, int cols) { return (lines + cols) * 128; }
 constexpr int kSmallThreads = 256;  // warp 0 TMA, 1 MMA, 2 TMEM, 4..7 adapters; all finish rows
 constexpr int kPartPitch = 132;     // floats per row of partial sums (528 bytes: spreads banks)
@@ -675,8 +677,8 @@ constexpr size_t kParts = 128 * kPartPitch * 4;
 template <int MODE, int ACT>
 __global__ void __launch_bounds__(kSmallThreads, 2)
 small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b0,
-             const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int splits,
-             const int a_lines) {
+             const __grid_constant__ CUtensorMap map_b1, const GemmArgs g, const int stages, const int per,
+             const int splits, const int a_lines) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSmallMaxStages], s_empty[kSmallMaxStages], s_done, s_xfull, s_xempty;
     __shared__ AdapterSmem s_ad;
@@ -755,71 +757,81 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                                                                                   : g.width * 128);
             const bool issue = tc::elect();
             bool ok = !*abort;
-            ok = __all_sync(0xffffffffu, ok);
             uint32_t issued = 0;
+            // (a lane whose wait gives up goes on without issuing: the warp's
+            // lanes keep the same way through the loop without a vote)
 #pragma unroll 1
-            for (int kb = kb0; kb < kb1 && ok; ++kb, at.next(stages), ++issued) {
-                if (at.pass > 0) {
-                    ok = __all_sync(0xffffffffu, tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort));
-                    if (!ok) break;
-                }
-                if (issue) {
-                    const uint32_t bar = smem_u32(&s_full[at.slot]), dst = smem + at.slot * stage;
-                    tc::arrive_tx(&s_full[at.slot], bytes);
-                    if (MODE == kInner) {
-                        for (int i = 0; i < slots; ++i)
-                            load_b<MODE, 1>(dst + b_at + i * lines * 128, &map_b0, &map_b1, g, kb,
-                                            s_ad.list[a0 + i], part * 128, bar);
-                    } else {
-                        // K-major: `width` lines in one box; MN-major: boxes of 64 columns
-                        load_b<MODE, 1>(dst + b_at, &map_b0, &map_b1, g, kb, n0, 0, bar);
-                        if (gated(MODE))
-                            load_b<MODE, 1>(dst + b_at + u_at * 128, &map_b0, &map_b1, g, kb, n0, 1, bar);
-                        if (b_mn(MODE) && g.width > 64)
-                            load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb, n0 + 64, 0, bar);
+            for (int kb = kb0; kb < kb1; kb += per, at.next(stages)) {
+                if (at.pass > 0) ok = ok && tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort);
+                if (issue && ok) {
+                    const uint32_t bar = smem_u32(&s_full[at.slot]);
+                    uint32_t dst = smem + at.slot * per * stage;
+                    const int two = per == 2 && kb + 1 < kb1;
+                    tc::arrive_tx(&s_full[at.slot], bytes << two);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j, dst += stage) {
+                        if (j > two) break;
+                        if (MODE == kInner) {
+                            for (int i = 0; i < slots; ++i)
+                                load_b<MODE, 1>(dst + b_at + i * lines * 128, &map_b0, &map_b1, g, kb + j,
+                                                s_ad.list[a0 + i], part * 128, bar);
+                        } else {
+                            // K-major: `width` lines in one box; MN-major: boxes of 64 columns
+                            load_b<MODE, 1>(dst + b_at, &map_b0, &map_b1, g, kb + j, n0, 0, bar);
+                            if (gated(MODE))
+                                load_b<MODE, 1>(dst + b_at + u_at * 128, &map_b0, &map_b1, g, kb + j, n0, 1, bar);
+                            if (b_mn(MODE) && g.width > 64)
+                                load_b<MODE, 1>(dst + b_at + tc::kBox, &map_b0, &map_b1, g, kb + j, n0 + 64, 0, bar);
+                        }
+                        load_a<MODE, 1>(dst, &map_a, g, kb + j, m0, half, a_lines / 64, bar);
                     }
-                    load_a<MODE, 1>(dst, &map_a, g, kb, m0, half, a_lines / 64, bar);
+                    ++issued;
                 }
                 __syncwarp();
             }
-            if (!ok)  // nothing in flight on the way out
-                for (uint32_t i = 0, left = min(issued, (uint32_t)stages); i < left; ++i) {
-                    const uint32_t back = i + 1;  // slots before the current one
-                    const bool wrapped = back > at.slot;
-                    mbar_wait(&s_full[wrapped ? at.slot + stages - back : at.slot - back],
-                              (wrapped ? at.pass - 1 : at.pass) & 1);
+            if (issue && !ok) {  // nothing in flight on the way out
+                const uint32_t total = (uint32_t)(kb1 - kb0 + per - 1) / per;
+                tc::Ring back = at;  // to the slot behind the last one issued
+                for (uint32_t i = issued; i < total; ++i) back.prev(stages);
+                for (uint32_t i = 0; i < min(issued, (uint32_t)stages); ++i) {
+                    back.prev(stages);
+                    mbar_wait(&s_full[back.slot], back.pass & 1);
                 }
+            }
             __syncwarp();
         } else if (warp == 1) {
             const uint32_t id = tc::idesc(128, g.cols, a_mn(MODE), b_mn(MODE));
             const uint64_t da0 = tc::desc<a_mn(MODE)>(smem), db0 = tc::desc<b_mn(MODE)>(smem + b_at);
             const bool issue = tc::elect();
             bool ok = !*abort;
-            ok = __all_sync(0xffffffffu, ok);
             int x = 0;
 #pragma unroll 1
-            for (int kb = kb0; kb < kb1 && ok; ++kb, at.next(stages)) {
-                ok = __all_sync(0xffffffffu, tc::wait(&s_full[at.slot], at.pass & 1, abort));
-                if (!ok) break;
+            for (int kb = kb0; kb < kb1; kb += per, at.next(stages)) {
+                ok = ok && tc::wait(&s_full[at.slot], at.pass & 1, abort);
                 tc::fence_after();
-                const uint64_t da = da0 + at.slot * (stage >> 4), db = db0 + at.slot * (stage >> 4);
-                if (issue) {
+                const uint64_t da = da0 + at.slot * per * (stage >> 4), db = db0 + at.slot * per * (stage >> 4);
+                if (issue && ok) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         tc::mma<1>(tmem, da + k * (tc::kstep<a_mn(MODE)>() >> 4),
                                    db + k * (tc::kstep<b_mn(MODE)>() >> 4), id, kb > kb0 || k > 0);
+                    if (per == 2 && kb + 1 < kb1)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma<1>(tmem, da + (stage >> 4) + k * (tc::kstep<a_mn(MODE)>() >> 4),
+                                       db + (stage >> 4) + k * (tc::kstep<b_mn(MODE)>() >> 4), id, true);
                     tc::commit<1>(&s_empty[at.slot]);
                 }
                 __syncwarp();
             }
             if (MODE == kProj && append) {
-                for (bool last = false; ok && !last; ++x) {
-                    ok = __all_sync(0xffffffffu, tc::wait(&s_xfull, x & 1, abort));
+                for (bool last = false; !last; ++x) {
+                    ok = __all_sync(0xffffffffu, ok && tc::wait(&s_xfull, x & 1, abort));
                     if (!ok) break;
                     tc::fence_after();
                     const int cmd = *(volatile int *)&s_ad.cmd;
                     last = cmd & 2;
-                    const uint64_t da = da0 + stages * (stage >> 4), db = db0 + stages * (stage >> 4);
+                    const uint64_t da = da0 + stages * per * (stage >> 4), db = db0 + stages * per * (stage >> 4);
                     if (issue) {
                         if (cmd & 1)
 #pragma unroll
@@ -860,7 +872,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             list_adapters(s_ad, g, m0, 128, tid);
             const int blocks = adapter_blocks(s_ad.count, g.rank);
             const int e0 = blocks * rank / splits, e1 = blocks * (rank + 1) / splits;
-            uint8_t *xa = base + stages * stage;
+            uint8_t *xa = base + stages * per * stage;
             AppendRow f;
             if (e0 < e1) fetch_block(f, s_ad, g, e0, m0, 0, n0, g.width, tid, true);
             int x = 0;
@@ -1046,12 +1058,12 @@ struct Plan {
 // the operands come from L2 (a pair's products keep up with that, 0.28 us per
 // block), about 45 where every byte comes from HBM; the share between is the
 // matrices' bytes over all that is loaded.  However few its bytes, a block
-// takes 0.2 us of issue and waits.
+// takes 0.15 us of issue and waits.
 double stream_us(int64_t ctas, int blocks, double stage, double once, int num_sms) {
     const double all = stage * blocks * (double)ctas, share = once < all ? once / all : 1.0;
     const double waves = (double)((ctas + num_sms - 1) / num_sms);
     const double block = stage * 1e-3 * (share / 45 + (1 - share) / 117);
-    return waves * blocks * (block > 0.2 ? block : 0.2);
+    return waves * blocks * (block > 0.15 ? block : 0.15);
 }
 
 // Pairs of CTAs with 256-row tiles, or single ones with a tile width and a
@@ -1151,18 +1163,20 @@ cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sm
     // them where there are more CTAs than SMs; beside one another, 70 KB for
     // kInner and twice that for the projection, whose K loop then runs meanwhile.
     size_t budget = ctas > num_sms ? kSmallSmem / 2 : kSmallSmem;
-    if (beside && !g.direct) budget = MODE == kInner ? 70 * 1024 : ctas > num_sms ? 70 * 1024 : 140 * 1024;
+    if (beside) budget = MODE == kInner ? 70 * 1024 : ctas > num_sms ? 70 * 1024 : 140 * 1024;
     // the products read 128 rows of A also where a stage holds fewer: room
     // behind the last stage keeps that inside the allocation
     const size_t tail = 2 * tc::kBox - lines * 128;
-    int slots = (int)((budget - tail) / stage);
-    if (slots > kSmallMaxStages) slots = kSmallMaxStages;
-    // one slot is for appended adapter blocks
-    const int stages = slots - (MODE == kProj && g.n > 0 && !g.direct ? 1 : 0);
-    size_t smem = (size_t)slots * stage + tail;
+    // one block is for appended adapters
+    const int extra = MODE == kProj && g.n > 0 && !g.direct ? 1 : 0;
+    const int blocks = (int)((budget - tail) / stage) - extra;
+    const int per = blocks >= 6 ? 2 : 1;  // K blocks per stage, three stages at least
+    int stages = blocks / per;
+    if (stages > kSmallMaxStages) stages = kSmallMaxStages;
+    size_t smem = (size_t)(per * stages + extra) * stage + tail;
     if (smem < kParts) smem = kParts;
     return launch_cluster(small_kernel<MODE, ACT>, (unsigned)ctas, kSmallThreads, smem + 1024,
-                          plan.splits > 1 ? plan.splits : 0, s, m.a, m.b0, m.b1, g, stages, plan.splits, lines);
+                          plan.splits > 1 ? plan.splits : 0, s, m.a, m.b0, m.b1, g, stages, per, plan.splits, lines);
 }
 
 template <int MODE, int ACT>
@@ -1194,9 +1208,10 @@ cudaError_t map_weight(CUtensorMap *m, const uint16_t *w, int64_t rows, int64_t 
 }
 
 template <int MODE, int ACT>
-cudaError_t launch_gemm(const Maps &m, const GemmArgs &g, const Plan &plan, int num_sms, cudaStream_t s) {
+cudaError_t launch_gemm(const Maps &m, const GemmArgs &g, const Plan &plan, int num_sms, cudaStream_t s,
+                        bool beside = false) {
     if (plan.pairs) return launch_big<MODE, ACT>(m, g, plan, num_sms, s);
-    return launch_small<MODE, ACT>(m, g, plan, num_sms, MODE == kProj && g.n > 0, s);
+    return launch_small<MODE, ACT>(m, g, plan, num_sms, beside, s);
 }
 
 template <int MODE>
@@ -1285,6 +1300,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     // plain projection's bits)
     const Plan plan = make_plan(kProj, g, num_sms, fill);
     Maps m;
+    bool beside = false;
     if (p.n > 0) {
         g.ids = p.ids;
         g.scale = p.scale;
@@ -1292,17 +1308,23 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.v = reinterpret_cast<uint16_t *>(p.v);
         g.n = p.n;
         g.rank = p.rank;
-        // Few tokens: inner products by plain loads, 1.25 x 2 T rank K bytes
-        // through L2 (about 6 TB/s) and 1.5 us for each time the SMs fill with
-        // CTAs, against about 8 us of kInner; v B^T as the rows are finished, 2 x
-        // width rank bytes per row of a CTA (16 per clock: every lane's load is
-        // a line of its own), against about 2 us of appended blocks.
+        // Inner products by plain loads, 2.5 T rank K bytes through L2 at about 6
+        // TB/s and 1.5 us for each time the SMs fill with CTAs; or by kInner, 6.5
+        // us and 0.4 per K block.  v B^T as the rows are finished: 2 x width rank
+        // bytes per row of a CTA (16 per clock: every lane's load is a line of
+        // its own), against about 2 us of appended blocks.
+        const int mt = ceil_div(p.T, 128);
+        int inner_splits = 1;
+        while (inner_splits < kMaxSplits && 2 * mt * inner_splits <= num_sms && g.kb / (2 * inner_splits) >= 4)
+            inner_splits *= 2;
         const double inner_us = 2.5 * p.T * (double)p.rank * p.K / 6e6 +
                                 1.5 * ceil_div((int64_t)p.T * p.rank / 4, 16 * num_sms);
         const double rows = (p.T < 128 ? p.T : 128) / (double)plan.splits;
         const double add_us = rows * plan.width * 2 * p.rank / 16 / 1900;
         g.direct = !plan.pairs && add_us < 2;
-        if (!plan.pairs && inner_us < 8) {
+        const bool plain = !plan.pairs && inner_us < 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
+        beside = !plan.pairs && !plain;
+        if (plain) {
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
         } else {
             const int lines = p.rank < 128 ? p.rank : 128;
@@ -1314,10 +1336,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
             // SMs that K splits leave go to clusters that share a row tile's
             // adapters (a split always has work, such a cluster may find none),
             // fewer adapters at a time if that gives each of them some
-            const int mt = ceil_div(p.T, 128);
-            Plan inner = {0, false, 1, 128, 128, 1};
-            while (inner.splits < kMaxSplits && 2 * mt * inner.splits <= num_sms && g.kb / (2 * inner.splits) >= 4)
-                inner.splits *= 2;
+            Plan inner = {0, false, inner_splits, 128, 128, 1};
             const int most = p.n < 128 ? p.n : 128;
             g.groups = num_sms / (mt * inner.splits);
             if (g.groups < 1) g.groups = 1;
@@ -1325,7 +1344,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
             inner.cols = (g.per_tile * lines + 15) / 16 * 16;
             const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
             if (g.groups > tiles) g.groups = tiles;
-            e = launch_small<kInner, 0>(m, g, inner, num_sms, !plan.pairs, s);
+            e = launch_small<kInner, 0>(m, g, inner, num_sms, beside, s);
             if (e != cudaSuccess) return e;
         }
     }
@@ -1334,7 +1353,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     m.b1 = m.b0;
     g.residual = p.residual;
     g.out0 = p.y;
-    return launch_gemm<kProj, 0>(m, g, plan, num_sms, s);
+    return launch_gemm<kProj, 0>(m, g, plan, num_sms, s, beside);
 }
 
 }  // namespace moe

@@ -142,6 +142,12 @@ struct Ring {
             ++pass;
         }
     }
+    __device__ __forceinline__ void prev(uint32_t n) {
+        if (slot-- == 0) {
+            slot = n - 1;
+            --pass;
+        }
+    }
 };
 
 // ---------------------------------------------------------------- cluster --
