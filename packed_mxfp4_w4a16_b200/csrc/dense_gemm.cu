@@ -1308,17 +1308,20 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.v = reinterpret_cast<uint16_t *>(p.v);
         g.n = p.n;
         g.rank = p.rank;
-        // Inner products by plain loads, 2.5 T rank K bytes through L2 at about 6
-        // TB/s and 1.5 us for each time the SMs fill with CTAs; or by kInner, 6.5
-        // us and 0.4 per K block.  v B^T as the rows are finished: 2 x width rank
-        // bytes per row of a CTA (16 per clock: every lane's load is a line of
-        // its own), against about 2 us of appended blocks.
+        // Inner products by plain loads: x once per four ranks and A once per token
+        // (2.5 T rank K bytes), or per up to four tokens of a run (1 to 2.5),
+        // through L2 at about 6 TB/s, and 2 us for each time the SMs fill with
+        // CTAs; or by kInner, 6.5 us and 0.4 per K block.  v B^T as the rows are
+        // finished: 2 x width rank bytes per row of a CTA (16 per clock: every
+        // lane's load is a line of its own), against about 2 us of appended blocks.
         const int mt = ceil_div(p.T, 128);
         int inner_splits = 1;
         while (inner_splits < kMaxSplits && 2 * mt * inner_splits <= num_sms && g.kb / (2 * inner_splits) >= 4)
             inner_splits *= 2;
-        const double inner_us = 2.5 * p.T * (double)p.rank * p.K / 6e6 +
-                                1.5 * ceil_div((int64_t)p.T * p.rank / 4, 16 * num_sms);
+        const int64_t ctas = (int64_t)p.T * p.rank / 4;
+        const double inner_us = ctas > 8 * num_sms
+                                    ? 1.6 * p.T * (double)p.rank * p.K / 6e6 + 2.0 * ceil_div(ctas / 4, 4 * num_sms)
+                                    : 2.5 * p.T * (double)p.rank * p.K / 6e6 + 2.0;
         const double rows = (p.T < 128 ? p.T : 128) / (double)plan.splits;
         const double add_us = rows * plan.width * 2 * p.rank / 16 / 1900;
         g.direct = !plan.pairs && add_us < 2;

@@ -232,69 +232,97 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
     if (threadIdx.x == 0 && s_abort) atomicOr(p.status, kTimeoutStatus);
 }
 
-// Inner products of few tokens: one CTA per token and RJ rank rows of its
-// adapter (x is read once for all RJ), 16-byte loads, FP32 sums.  Tokens of the
-// same adapter read its rows through L2 again; from about 8 us of that on the
-// tensor-core form is the faster one.
+// Inner products by plain loads: one CTA per TT tokens and RJ rank rows (x is
+// read once for all RJ).  It takes the tokens in runs that name the same
+// adapter, whose rows are read once for the run.
 constexpr int kInnerThreads = 128;
-template <int RJ, bool BF16>
+template <int RJ, int TT, bool BF16>
 __global__ void __launch_bounds__(kInnerThreads)
 inner_kernel(const AdapterParams p) {
-    __shared__ float red[kInnerThreads / 32][RJ];
+    __shared__ float red[kInnerThreads / 32][TT * RJ];
     pdl_wait();
     pdl_launch_dependents();
     const int groups = (p.rank + RJ - 1) / RJ;
-    const int j0 = blockIdx.x % groups * RJ, t = blockIdx.x / groups, id = p.ids[t];
-    if (id < 0 || id >= p.n) {
-        if (threadIdx.x == 0 && j0 == 0 && id != -1) atomicOr(p.status, kBadAdapterStatus);
-        return;  // v of a token without an adapter is not read
-    }
-    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + (size_t)t * p.K);
-    const uint4 *a = reinterpret_cast<const uint4 *>(p.a + ((size_t)id * p.rank + j0) * p.K);
-    const int chunks = p.K / 8;  // per row
-    float s[RJ] = {};
-#pragma unroll 2
-    for (int c = threadIdx.x; c < chunks; c += kInnerThreads) {
-        const uint4 xv = __ldg(x + c);
-        uint4 av[RJ];
+    const int j0 = blockIdx.x % groups * RJ, t0 = blockIdx.x / groups * TT;
+    int ids[TT];
 #pragma unroll
-        for (int j = 0; j < RJ; ++j) av[j] = __ldg(a + (size_t)j * chunks + c);
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int j = 0; j < RJ; ++j) {
-            const uint32_t aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                s[j] = fmaf(bf16_to_f32(xw[h] & 0xFFFFu), bf16_to_f32(aw[h] & 0xFFFFu), s[j]);
-                s[j] = fmaf(bf16_to_f32(xw[h] >> 16), bf16_to_f32(aw[h] >> 16), s[j]);
-            }
+    for (int i = 0; i < TT; ++i) {
+        ids[i] = t0 + i < p.T ? p.ids[t0 + i] : -1;
+        if (ids[i] < -1 || ids[i] >= p.n) {
+            if (threadIdx.x == 0 && j0 == 0) atomicOr(p.status, kBadAdapterStatus);
+            ids[i] = -1;
         }
     }
+    const int chunks = p.K / 8;  // per row
+#pragma unroll 1
+    for (int first = 0; first < TT;) {
+        int id = -1, count = 0;  // the run that starts at `first`
 #pragma unroll
-    for (int j = 0; j < RJ; ++j) {
-        s[j] = warp_sum(s[j]);
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][j] = s[j];
-    }
-    __syncthreads();
-    if (threadIdx.x < RJ) {
-        float v = 0.f;
+        for (int i = 0; i < TT; ++i) {
+            if (i == first) id = ids[i];
+            if (i == first + count && ids[i] == id) ++count;
+        }
+        const int t = t0 + first;
+        first += count;
+        if (id < 0) continue;  // v of a token without an adapter is not read
+        const uint4 *a = reinterpret_cast<const uint4 *>(p.a + ((size_t)id * p.rank + j0) * p.K);
+        // (tokens past the run repeat its last one; their sums are not written)
+        const uint4 *x[TT];
 #pragma unroll
-        for (int w = 0; w < kInnerThreads / 32; ++w) v += red[w][threadIdx.x];
-        v *= p.scale[id];
-        const size_t o = (size_t)t * p.rank + j0 + threadIdx.x;
-        if (BF16)
-            reinterpret_cast<uint16_t *>(p.v)[o] = f32_to_bf16(v);
-        else
-            p.v[o] = v;
+        for (int i = 0; i < TT; ++i)
+            x[i] = reinterpret_cast<const uint4 *>(p.x + (size_t)(t + min(i, count - 1)) * p.K);
+        float s[TT][RJ] = {};
+#pragma unroll 2
+        for (int c = threadIdx.x; c < chunks; c += kInnerThreads) {
+            uint4 av[RJ], xv[TT];
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) av[j] = __ldg(a + (size_t)j * chunks + c);
+#pragma unroll
+            for (int i = 0; i < TT; ++i) xv[i] = __ldg(x[i] + c);
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+                if (i >= count) break;
+                const uint32_t xw[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+#pragma unroll
+                for (int j = 0; j < RJ; ++j) {
+                    const uint32_t aw[4] = {av[j].x, av[j].y, av[j].z, av[j].w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        s[i][j] = fmaf(bf16_to_f32(xw[h] & 0xFFFFu), bf16_to_f32(aw[h] & 0xFFFFu), s[i][j]);
+                        s[i][j] = fmaf(bf16_to_f32(xw[h] >> 16), bf16_to_f32(aw[h] >> 16), s[i][j]);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // red[] of the run before has been read
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) {
+                s[i][j] = warp_sum(s[i][j]);
+                if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5][i * RJ + j] = s[i][j];
+            }
+        __syncthreads();
+        if (threadIdx.x < count * RJ) {
+            float v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kInnerThreads / 32; ++w) v += red[w][threadIdx.x];
+            v *= p.scale[id];
+            const size_t o = (size_t)(t + threadIdx.x / RJ) * p.rank + j0 + threadIdx.x % RJ;
+            if (BF16)
+                reinterpret_cast<uint16_t *>(p.v)[o] = f32_to_bf16(v);
+            else
+                p.v[o] = v;
+        }
     }
 }
 
-template <int RJ, bool BF16>
+template <int RJ, int TT, bool BF16>
 cudaError_t launch_inner_v(const AdapterParams &p, cudaStream_t s) {
     static PerDeviceOnce once;
-    const cudaError_t e = per_device_once(once, [] { return smem_attributes(inner_kernel<RJ, BF16>, 0); });
+    const cudaError_t e = per_device_once(once, [] { return smem_attributes(inner_kernel<RJ, TT, BF16>, 0); });
     if (e != cudaSuccess) return e;
-    return launch_ex(inner_kernel<RJ, BF16>, dim3(p.T * ((p.rank + RJ - 1) / RJ)), dim3(kInnerThreads), 0, s, true, p);
+    return launch_ex(inner_kernel<RJ, TT, BF16>, dim3((p.T + TT - 1) / TT * ((p.rank + RJ - 1) / RJ)), dim3(kInnerThreads), 0, s, true, p);
 }
 
 constexpr size_t kSmemMost = 220 * 1024;
@@ -357,13 +385,15 @@ cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s)
     return launch_gemv<true, MOE_ACT_GELU_TANH>(g, num_sms, s);
 }
 
-// v in FP32 (read by gemv_kernel) or BF16 (by the tensor-core projection).
-// rank is a multiple of 8: four rank rows per CTA, or one where those leave
-// SMs idle.
+// v in FP32 (read by gemv_kernel, up to 8 tokens) or BF16 (by the tensor-core
+// projection).  rank is a multiple of 8: four rank rows per CTA, one where those
+// leave SMs idle; four tokens where single ones would fill the SMs several
+// times over.
 cudaError_t launch_inner(const AdapterParams &p, bool bf16, int num_sms, cudaStream_t s) {
-    if ((int64_t)p.T * (p.rank / 4) >= num_sms)
-        return bf16 ? launch_inner_v<4, true>(p, s) : launch_inner_v<4, false>(p, s);
-    return bf16 ? launch_inner_v<1, true>(p, s) : launch_inner_v<1, false>(p, s);
+    const int64_t ctas = (int64_t)p.T * (p.rank / 4);
+    if (!bf16) return ctas >= num_sms ? launch_inner_v<4, 1, false>(p, s) : launch_inner_v<1, 1, false>(p, s);
+    if (ctas > 8 * num_sms) return launch_inner_v<4, 4, true>(p, s);
+    return ctas >= num_sms ? launch_inner_v<4, 1, true>(p, s) : launch_inner_v<1, 1, true>(p, s);
 }
 
 cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s) {
