@@ -48,6 +48,9 @@ int device_info(int *dev, DeviceInfo *out) {
     return MOE_OK;
 }
 
+// Row indices (with a tile's rows past the last one) stay inside an int.
+constexpr int kMaxTokens = 1 << 30;
+bool tokens_ok(int T) { return T >= 0 && T <= kMaxTokens; }
 bool dim_ok(int v) { return v >= 8 && v <= 65536 && v % 8 == 0; }
 
 struct Range {
@@ -82,7 +85,7 @@ extern "C" {
 int moe_gated_ffn(const uint16_t *x, int T, int H, int I, const uint16_t *w_gate,
                   const uint16_t *w_up, int act, unsigned flags, uint16_t *x_norm, uint16_t *h,
                   void *stream) {
-    if (T < 0 || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
+    if (!tokens_ok(T) || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
     if (act < MOE_ACT_SILU || act > MOE_ACT_GELU_TANH || (flags & ~MOE_FFN_RMSNORM)) return MOE_ERR_ARG;
     const bool norm = flags & MOE_FFN_RMSNORM;
     if (norm != (x_norm != nullptr) && T > 0) return MOE_ERR_ARG;
@@ -113,7 +116,7 @@ int moe_gated_ffn(const uint16_t *x, int T, int H, int I, const uint16_t *w_gate
 }
 
 int moe_gated_ffn_backward_workspace_bytes(int T, int H, int I, size_t *bytes) {
-    if (!bytes || T < 0 || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
+    if (!bytes || !tokens_ok(T) || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
     *bytes = moe::align_up(2 * bf16_bytes(T > 0 ? T : 1, I), 256);
     return MOE_OK;
 }
@@ -122,7 +125,7 @@ int moe_gated_ffn_backward(const uint16_t *x, int T, int H, int I, const uint16_
                            const uint16_t *w_up, int act, const uint16_t *dh, uint16_t *dx,
                            uint16_t *dw_gate, uint16_t *dw_up, void *workspace, size_t bytes,
                            void *stream) {
-    if (T < 0 || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
+    if (!tokens_ok(T) || !dim_ok(H) || !dim_ok(I)) return MOE_ERR_ARG;
     if (act < MOE_ACT_SILU || act > MOE_ACT_GELU_TANH) return MOE_ERR_ARG;
     if ((dw_gate == nullptr) != (dw_up == nullptr)) return MOE_ERR_ARG;
     if (T > 0 && !dx && !dw_gate) return MOE_ERR_ARG;
@@ -171,7 +174,7 @@ int moe_gated_ffn_backward(const uint16_t *x, int T, int H, int I, const uint16_
 }
 
 int moe_adapter_proj_workspace_bytes(int T, int K, int N, int n_adapters, int rank, size_t *bytes) {
-    if (!bytes || T < 0 || !dim_ok(K) || !dim_ok(N) || n_adapters < 0) return MOE_ERR_ARG;
+    if (!bytes || !tokens_ok(T) || !dim_ok(K) || !dim_ok(N) || n_adapters < 0) return MOE_ERR_ARG;
     if (n_adapters > 0 && (rank < 8 || rank > 256 || rank % 8)) return MOE_ERR_ARG;
     *bytes = n_adapters > 0 ? moe::adapter_workspace(T > 0 ? T : 1, K, N, n_adapters, rank) : 0;
     return MOE_OK;

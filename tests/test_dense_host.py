@@ -22,7 +22,7 @@ X, WG, WU, H_, XN, DH, DX, DG, DU, WS = (C.c_void_p(0x10000000 * (i + 1)) for i 
 def test_gated_ffn_refusals(lib):
     def call(x=X, T=4, H=64, I=32, wg=WG, wu=WU, act=0, flags=0, xn=None, h=H_):
         return lib.moe_gated_ffn(x, T, H, I, wg, wu, act, flags, xn, h, None)
-    for bad in (dict(T=-1), dict(H=0), dict(H=12), dict(H=65544), dict(I=4), dict(I=-8), dict(act=3),
+    for bad in (dict(T=-1), dict(T=2 ** 30 + 1), dict(H=0), dict(H=12), dict(H=65544), dict(I=4), dict(I=-8), dict(act=3),
                 dict(act=-1), dict(flags=2), dict(flags=1), dict(xn=XN), dict(h=X), dict(h=WG), dict(h=WU),
                 dict(flags=1, xn=H_), dict(flags=1, xn=X), dict(h=C.c_void_p(X.value + 16))):
         assert call(**bad) == ARG, bad
@@ -33,7 +33,7 @@ def test_gated_ffn_refusals(lib):
 def test_backward_refusals(lib):
     def call(x=X, T=4, H=64, I=32, wg=WG, wu=WU, act=0, dh=DH, dx=DX, dg=DG, du=DU, ws=WS, n=1 << 20):
         return lib.moe_gated_ffn_backward(x, T, H, I, wg, wu, act, dh, dx, dg, du, ws, n, None)
-    for bad in (dict(T=-1), dict(H=4), dict(I=20), dict(act=7), dict(dg=None), dict(du=None),
+    for bad in (dict(T=-1), dict(T=2 ** 31 - 1), dict(H=4), dict(I=20), dict(act=7), dict(dg=None), dict(du=None),
                 dict(dx=None, dg=None, du=None), dict(dx=X), dict(dg=DU), dict(du=WU), dict(dx=DH),
                 dict(ws=X), dict(ws=DX), dict(T=0, dg=DG, du=DG)):
         assert call(**bad) == ARG, bad
@@ -54,7 +54,7 @@ def test_adapter_refusals(lib):
     def call(x=X, T=4, K=64, N=32, w=WG, res=None, n=2, rank=8, a=a, b=b, s=s, ids=ids, y=y, ws=WS,
              size=1 << 20):
         return lib.moe_adapter_proj(x, T, K, N, w, res, n, rank, a, b, s, ids, y, ws, size, None)
-    for bad in (dict(T=-1), dict(K=60), dict(N=4), dict(n=-1), dict(rank=0), dict(rank=12),
+    for bad in (dict(T=-1), dict(T=2 ** 30 + 1), dict(K=60), dict(N=4), dict(n=-1), dict(rank=0), dict(rank=12),
                 dict(rank=264), dict(n=0), dict(y=X), dict(y=WG), dict(y=a), dict(y=b), dict(y=WS),
                 dict(res=C.c_void_p(y.value + 16)), dict(res=WS), dict(ws=X), dict(ws=ids)):
         assert call(**bad) == ARG, bad

@@ -1,12 +1,15 @@
 """Dense layers as they are used: DenseFFN, stacks of dense and MoE layers, CUDA
 graphs, streams, calls that share or must not share buffers."""
-import numpy as np
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import packed_mxfp4_w4a16_b200 as moe
 from dense_util import adapter64, assert_within, gated64, gated_backward64, normal
-from gpu_util import dev_bf16, dev_layer
+from gpu_util import dev_layer
 from workloads import synth
 
 pytestmark = pytest.mark.gpu
@@ -244,3 +247,37 @@ def test_memory_of_another_device_is_refused():
     w = normal((72, 136), 0.1, 4)
     with pytest.raises(moe.MoEError):
         moe.moe_gated_ffn(normal((20, 136), 1, 3, device="cuda:1"), w, w)
+
+
+FIRST_CALL = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import packed_mxfp4_w4a16_b200 as moe
+T = {T}
+n = lambda *s: torch.randn(*s, device="cuda").to(torch.bfloat16)
+x, wg, wu, dh, wd = n(T, 512), n(264, 512), n(264, 512), n(T, 264), n(512, 264)
+a, b, sc = n(3, 16, 264), n(3, 512, 16), torch.ones(3, device="cuda")
+ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+
+def run():
+    h = moe.moe_gated_ffn(x, wg, wu)
+    y = moe.moe_adapter_proj(h, wd, a, b, sc, ids, residual=x)
+    return [h, y, *moe.moe_gated_ffn_backward(x, wg, wu, dh)]
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(out, run()))
+assert moe.moe_dense_status() == 0
+"""
+
+
+@pytest.mark.parametrize("T", [1, 30, 4000])
+def test_first_call_of_a_process_may_be_captured(T):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=root, T=T)], capture_output=True, text=True,
+                       timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
