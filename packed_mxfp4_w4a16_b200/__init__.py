@@ -362,8 +362,7 @@ def moe_stack_set_spin_limit(s: int, polls: int) -> None:
 
 # ------------------------------------------- dense feed-forward layers
 # A call at small sizes is a few microseconds on the GPU, so the checks below
-# are written to cost little: plain conditions first, the names of what failed
-# only on the way to the error.
+# are written to cost little.
 
 _BF16 = torch.bfloat16
 
@@ -373,14 +372,6 @@ def _is(t, dtype, shape):
     pointers and cannot check sizes; they refuse host memory and other
     devices)."""
     return t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
-def _expect(name, **wants):
-    """Raise MoEError naming the first of what=(tensor, dtype, shape) that is
-    not as wanted."""
-    for what, (t, dtype, shape) in wants.items():
-        if not _is(t, dtype, shape):
-            raise MoEError(f"{name} ({what})", -1)
 
 
 def _new(like, shape, stream):
@@ -416,12 +407,15 @@ def _ptr(t):
 
 
 def _gated_shapes(x, w_gate, w_up, name):
-    if x is None or x.dim() != 2 or w_gate is None or w_gate.dim() != 2:
-        raise MoEError(f"{name} (shape)", -1)
-    (T, H), I = x.shape, w_gate.shape[0]
-    wshape = (I, H)
-    if not (_is(x, _BF16, (T, H)) and _is(w_gate, _BF16, wshape) and _is(w_up, _BF16, wshape)):
-        _expect(name, x=(x, _BF16, (T, H)), w_gate=(w_gate, _BF16, wshape), w_up=(w_up, _BF16, wshape))
+    try:
+        (T, H), (I, K) = x.shape, w_gate.shape
+        ok = (H == K and w_up.shape == w_gate.shape and x.dtype is _BF16 and w_gate.dtype is _BF16
+              and w_up.dtype is _BF16 and x.is_contiguous() and w_gate.is_contiguous()
+              and w_up.is_contiguous())
+    except (AttributeError, ValueError):  # None, or not two dimensions
+        ok = False
+    if not ok:
+        raise MoEError(f"{name} (x [T, H], w_gate and w_up [I, H]: BF16, contiguous)", -1)
     return T, H, I
 
 
@@ -472,7 +466,8 @@ def moe_gated_ffn_backward(x, w_gate, w_up, dh, act=ACT_SILU, dx=None, dw_gate=N
             dw_gate = _new(w_gate, (I, H), stream)
         if dw_up is None:
             dw_up = _new(w_up, (I, H), stream)
-        _expect(name, dw_gate=(dw_gate, _BF16, (I, H)), dw_up=(dw_up, _BF16, (I, H)))
+        if not (_is(dw_gate, _BF16, (I, H)) and _is(dw_up, _BF16, (I, H))):
+            raise MoEError(f"{name} (dw_gate or dw_up)", -1)
     workspace = _workspace(workspace, moe_gated_ffn_backward_workspace_bytes(T, H, I), x, name,
                            stream)
     check(name, load().moe_gated_ffn_backward(
@@ -497,22 +492,29 @@ def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_id
     adapter_ids int32 [T]. All four adapter arguments None: the plain
     projection. residual may be y. Returns y BF16 [T, N]."""
     name = "moe_adapter_proj"
-    if x is None or x.dim() != 2 or w is None or w.dim() != 2:
-        raise MoEError(f"{name} (shape)", -1)
-    (T, K), N = x.shape, w.shape[0]
-    if not (_is(x, _BF16, (T, K)) and _is(w, _BF16, (N, K))):
-        _expect(name, x=(x, _BF16, (T, K)), w=(w, _BF16, (N, K)))
+    try:
+        (T, K), (N, L) = x.shape, w.shape
+        ok = (K == L and x.dtype is _BF16 and w.dtype is _BF16 and x.is_contiguous()
+              and w.is_contiguous())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        raise MoEError(f"{name} (x [T, K], w [N, K]: BF16, contiguous)", -1)
     n = rank = need = 0
     pa = pb = ps = pi = pw = None
     if lora_a is not None:
-        if lora_a.dim() != 3 or lora_a.shape[0] == 0:
-            raise MoEError(f"{name} (adapters)", -1)
-        n, rank, _ = lora_a.shape
-        if not (_is(lora_a, _BF16, (n, rank, K)) and _is(lora_b, _BF16, (n, N, rank))
-                and _is(lora_scale, torch.float32, (n,)) and _is(adapter_ids, torch.int32, (T,))):
-            _expect(name, lora_a=(lora_a, _BF16, (n, rank, K)), lora_b=(lora_b, _BF16, (n, N, rank)),
-                    lora_scale=(lora_scale, torch.float32, (n,)),
-                    adapter_ids=(adapter_ids, torch.int32, (T,)))
+        try:
+            n, rank, L = lora_a.shape
+            ok = (n > 0 and L == K and lora_b.shape == (n, N, rank) and lora_scale.shape == (n,)
+                  and adapter_ids.shape == (T,) and lora_a.dtype is _BF16 and lora_b.dtype is _BF16
+                  and lora_scale.dtype is torch.float32 and adapter_ids.dtype is torch.int32
+                  and lora_a.is_contiguous() and lora_b.is_contiguous()
+                  and lora_scale.is_contiguous() and adapter_ids.is_contiguous())
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            raise MoEError(f"{name} (lora_a [n, rank, K], lora_b [n, N, rank] BF16, lora_scale [n] "
+                           "FP32, adapter_ids [T] int32, contiguous)", -1)
         pa, pb, ps, pi = (lora_a.data_ptr(), lora_b.data_ptr(), lora_scale.data_ptr(),
                           adapter_ids.data_ptr())
         workspace = _workspace(workspace, moe_adapter_proj_workspace_bytes(T, K, N, n, rank), x,
@@ -644,7 +646,8 @@ class DenseFFN:
         moe_device_check()
         _gated_shapes(w_gate, w_gate, w_up, "DenseFFN")
         self.I, self.H = w_gate.shape
-        _expect("DenseFFN", w_down=(w_down, _BF16, (self.H, self.I)))
+        if not _is(w_down, _BF16, (self.H, self.I)):
+            raise MoEError("DenseFFN (w_down)", -1)
         self.w_gate, self.w_up, self.w_down, self.act, self.lora = w_gate, w_up, w_down, act, lora
         self.max_tokens = max_tokens
         self.h = w_gate.new_empty(max_tokens, self.I)
