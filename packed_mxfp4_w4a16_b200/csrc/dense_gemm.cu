@@ -33,6 +33,7 @@ struct GemmArgs {
     int kb, kb_half;           // K blocks of 64; kDx: of one half
     int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
     int n_fast;                // consecutive tiles share M (else N)
+    int wide;                  // outputs allow 32-byte stores
     int width, cols;           // small_kernel: output columns per tile, columns of its products
     // adapters (kProj with n > 0, kInner)
     const int32_t *ids;        // [M]
@@ -93,7 +94,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f32(uint32_t w) { return bf16_to_f32(w & 0xFFFFu); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// W neighbouring BF16 (4: 8 bytes, 8: 16 bytes) as words.
+// W neighbouring BF16 (4: 8 bytes, 8: 16 bytes, 16: 32 bytes) as words.
 template <int W>
 struct Words {
     uint32_t w[W / 2];
@@ -101,22 +102,35 @@ struct Words {
 template <int W>
 __device__ __forceinline__ Words<W> load_words(const uint16_t *p) {
     Words<W> r;
-    if (W == 8) {
-        const uint4 d = *reinterpret_cast<const uint4 *>(p);
-        r.w[0] = d.x, r.w[1] = d.y, r.w[W / 2 - 2] = d.z, r.w[W / 2 - 1] = d.w;
-    } else {
+    if (W == 4) {
         const uint2 d = *reinterpret_cast<const uint2 *>(p);
         r.w[0] = d.x, r.w[1] = d.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W / 8; ++i) {
+            const uint4 d = *reinterpret_cast<const uint4 *>(p + 8 * i);
+            r.w[4 * i] = d.x, r.w[4 * i + 1] = d.y, r.w[(4 * i + 2) % (W / 2)] = d.z, r.w[(4 * i + 3) % (W / 2)] = d.w;
+        }
     }
     return r;
 }
+// W = 16: one 32-byte store (p 32-byte aligned).  A lane that owns a row writes
+// a whole sector that way (with two 16-byte stores the backward pass of T 2048,
+// H 2048, I 1536 took 69.1 us instead of 65.2).
 template <int W>
 __device__ __forceinline__ void store_bf16(uint16_t *p, const float (&v)[W]) {
-    if (W == 8)
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[W - 4], v[W - 3]),
-                                                   pack2(v[W - 2], v[W - 1]));
+    uint32_t w[W / 2];
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+    if (W == 16)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1 % (W / 2)]),
+                     "r"(w[2 % (W / 2)]), "r"(w[3 % (W / 2)]), "r"(w[4 % (W / 2)]), "r"(w[5 % (W / 2)]),
+                     "r"(w[6 % (W / 2)]), "r"(w[7 % (W / 2)])
+                     : "memory");
+    else if (W == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2 % (W / 2)], w[3 % (W / 2)]);
     else
-        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
 // What the outputs at (row, n ..) need besides the sums: dh or the residual.
@@ -376,6 +390,20 @@ __device__ __forceinline__ void add_direct(const GemmArgs &g, int64_t row, int n
     }
 }
 
+// W neighbouring sums of a row, as read from TMEM, to the outputs.
+template <int MODE, int ACT, int W>
+__device__ __forceinline__ void finish_row(const GemmArgs &g, bool bad, int64_t row, int half, int n,
+                                           const uint32_t (&v)[W], const uint32_t (&u)[W]) {
+    float fv[W], fu[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        fv[i] = __uint_as_float(v[i]);
+        fu[i] = gated(MODE) ? __uint_as_float(u[i]) : 0.f;
+    }
+    if (MODE == kProj && bad) add_left_out<W>(g, row, n, fv);
+    finish<MODE, ACT, W>(g, row, half, n, fv, fu, side_words<MODE, W>(g, row, n));
+}
+
 // ------------------------------------------------------- large products --
 // A pair of CTAs (cluster of 2, cta_group::2) owns 256 x `cols` accumulators
 // (cols up to 256, fewer where that leaves fewer SMs without a tile at the end):
@@ -619,18 +647,15 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 if (gated(MODE)) tc::tmem_ld16(acc + half_cols + c, u);
                 tc::tmem_wait();
                 if (m < g.M) {
+                    if (g.wide && n + c + 16 <= g.N) {
+                        finish_row<MODE, ACT, 16>(g, adapters && *(volatile int *)&s_ad.bad, m, half, n + c, v, u);
+                    } else {
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        if (n + c + 8 * q >= g.N) break;
-                        float fv[8], fu[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            fv[i] = __uint_as_float(v[8 * q + i]);
-                            fu[i] = gated(MODE) ? __uint_as_float(u[8 * q + i]) : 0.f;
-                        }
-                        if (MODE == kProj && adapters && *(volatile int *)&s_ad.bad)
-                            add_left_out<8>(g, m, n + c + 8 * q, fv);
-                        finish<MODE, ACT, 8>(g, m, half, n + c + 8 * q, fv, fu, side_words<MODE, 8>(g, m, n + c + 8 * q));
+                        for (int q = 0; q < 2; ++q)
+                            if (n + c + 8 * q < g.N)
+                                finish_row<MODE, ACT, 8>(g, adapters && *(volatile int *)&s_ad.bad, m, half,
+                                                         n + c + 8 * q, *reinterpret_cast<uint32_t(*)[8]>(v + 8 * q),
+                                                         *reinterpret_cast<uint32_t(*)[8]>(u + 8 * q));
                     }
                 }
             }
@@ -1192,6 +1217,7 @@ cudaError_t launch_big(const Maps &m, GemmArgs g, const Plan &plan, int num_sms,
     g.width = plan.width;
     g.cols = plan.cols;
     g.n_fast = g.nt < g.mt;
+    g.wide = g.N % 16 == 0 && ((uintptr_t)g.out0 | (uintptr_t)g.out1) % 32 == 0;
     const int64_t tiles = (int64_t)g.mt * g.nt;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
