@@ -1107,24 +1107,28 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
         if (p.us < 0.97 * best.us) best = p;
     }
     const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
-    // joining the parts of a split K: about 2 us, more for larger clusters
-    const double join[4] = {0, 2.5, 3, 3.5};
     for (int l = 0; l < 4; ++l) {
         const int splits = 1 << l;
         if (l > 0 && g.kb / splits < 4) break;
-        Plan p = {0, false, splits, most, 0, 0};
         const int64_t room = fill.ctas[l] / (mt * splits);  // tiles along N that run at once
-        if (b_mn(mode)) {
-            if (ceil_div(g.N, 64) <= room) p.width = 64;
-        } else if (room > ceil_div(g.N, most)) {
-            p.width = (ceil_div(g.N, room) + 3) / 4 * 4;
-            if (p.width < 8) p.width = 8;
+        for (int narrow = 0; narrow < 2; ++narrow) {
+            Plan p = {0, false, splits, most, 0, 0};
+            if (narrow && b_mn(mode)) {
+                p.width = 64;
+            } else if (narrow) {
+                if (room <= ceil_div(g.N, most)) break;
+                p.width = (ceil_div(g.N, room) + 3) / 4 * 4;
+                if (p.width < 8) p.width = 8;
+            }
+            p.cols = gated(mode) ? (p.width + 7) / 8 * 16 : (p.width + 15) / 16 * 16;
+            p.nt = ceil_div(g.N, p.width);
+            const double stage = small_stage(a_lines(mode, g.M), p.cols);
+            p.us = stream_us(mt * p.nt * splits, ceil_div(g.kb, splits), stage, once, fill.ctas[l]);
+            // joining the parts of a split K: the barriers, and about 20 bytes per
+            // ns into a CTA through distributed shared memory
+            if (l > 0) p.us += 1.2 + (g.M < 128 ? g.M : 128) * p.cols * 4 / 20e3;
+            if (p.us < best.us) best = p;
         }
-        p.cols = gated(mode) ? (p.width + 7) / 8 * 16 : (p.width + 15) / 16 * 16;
-        p.nt = ceil_div(g.N, p.width);
-        const double stage = small_stage(a_lines(mode, g.M), p.cols);
-        p.us = join[l] + stream_us(mt * p.nt * splits, ceil_div(g.kb, splits), stage, once, fill.ctas[l]);
-        if (p.us < best.us) best = p;
     }
     return best;
 }
