@@ -45,7 +45,8 @@ struct GemmArgs {
     // free, which lets it start only after its own wait, and waits for it at its end.
     int late;
     int n, rank;
-    int direct;                // small_kernel adds v B^T as it finishes rows
+    int direct;                // small_kernel: v B^T by plain products beside the K loop,
+                               // left at this offset in shared memory (0: not)
     int per_tile, parts;       // kInner: adapters per 128 columns, or tiles per adapter
     int groups;                // kInner: CTAs (clusters) that share a row tile's adapters
 };
@@ -256,7 +257,7 @@ __device__ __forceinline__ void list_adapters(AdapterSmem &s, const GemmArgs &g,
     group_sync();
 }
 
-__device__ __forceinline__ int adapter_blocks(int count, int rank) {
+__host__ __device__ __forceinline__ int adapter_blocks(int count, int rank) {
     if (rank > 64) return count * ((rank + 63) / 64);
     const int per = 64 / rank;
     return (count + per - 1) / per;
@@ -363,30 +364,66 @@ __device__ __forceinline__ void add_left_out(const GemmArgs &g, int64_t row, int
     for (int i = 0; i < W; ++i) v[i] = s.v[i];
 }
 
-// v B^T of row `row`, added to outputs n .. n + 3 (the form for few tokens: a
-// row reads the B rows of its own adapter only, from L2).
-__device__ __forceinline__ void add_direct(const GemmArgs &g, int64_t row, int n, float (&acc)[4]) {
-    const int id = g.ids[row];
-    if (id < 0 || id >= g.n) return;
-    const uint4 *v = reinterpret_cast<const uint4 *>(g.v + row * g.rank);
-    const uint4 *b = reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)id * g.N + n) * g.rank);
-    const int chunks = g.rank / 8;
-#pragma unroll 2
-    for (int c = 0; c < chunks; ++c) {
-        const uint4 vv = v[c];
-        uint4 bv[4];
+// v B^T by plain FP32 products, for few rows per CTA: each row reads the B rows
+// of its own adapter only.  128 threads that are idle during the K loop take
+// four outputs of a row at a time, two such groups together, and leave them in
+// `delta` ([rows][width] in shared memory) for the finishing threads.
+__device__ __forceinline__ void dot8(const uint4 &x, const uint4 &y, float &acc) {
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) bv[i] = __ldg(b + i * chunks + c);
-        const uint32_t vw[4] = {vv.x, vv.y, vv.z, vv.w};
+    for (int h = 0; h < 4; ++h) {
+        acc = fmaf(lo_f32(xw[h]), lo_f32(yw[h]), acc);
+        acc = fmaf(hi_f32(xw[h]), hi_f32(yw[h]), acc);
+    }
+}
+__device__ __forceinline__ void direct_products(const GemmArgs &g, int m0, int r0, int r1, int n0, int tid,
+                                                float *delta) {
+    const int per_row = g.width / 4, items = (r1 - r0) * per_row, chunks = g.rank / 8;
+    bool waited = false;
+#pragma unroll 1
+    for (int i0 = tid; i0 < items || !waited; i0 += 2 * kGroup) {
+        const uint4 *v[2], *b[2];
+        float acc[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t bw[4] = {bv[i].x, bv[i].y, bv[i].z, bv[i].w};
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                acc[i] = fmaf(lo_f32(vw[h]), lo_f32(bw[h]), acc[i]);
-                acc[i] = fmaf(hi_f32(vw[h]), hi_f32(bw[h]), acc[i]);
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * kGroup, t = m0 + r0 + i / per_row, n = n0 + i % per_row * 4;
+            const int id = i < items && n < g.N ? g.ids[t] : -1;
+            v[k] = b[k] = nullptr;
+            if (id >= 0 && id < g.n) {
+                v[k] = reinterpret_cast<const uint4 *>(g.v + (size_t)t * g.rank);
+                b[k] = reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)id * g.N + n) * g.rank);
             }
         }
+#pragma unroll 1
+        for (int c0 = 0; c0 < chunks; c0 += 2) {
+            uint4 vv[2][2], bv[2][2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (v[k] && c0 + c < chunks)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) bv[k][c][j] = __ldg(b[k] + j * chunks + c0 + c);
+            if (!waited) pdl_wait();  // v; the first of B is on its way
+            waited = true;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (v[k] && c0 + c < chunks) vv[k][c] = v[k][c0 + c];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    if (v[k] && c0 + c < chunks)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dot8(vv[k][c], bv[k][c][j], acc[k][j]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (i0 + k * kGroup < items)
+                *reinterpret_cast<float4 *>(delta + 4 * (i0 + k * kGroup)) =
+                    make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
     }
 }
 
@@ -892,6 +929,8 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(
                             reinterpret_cast<const uint8_t *>(g.lora_b + ((size_t)id * g.N + n0) * g.rank) + b));
             }
+            direct_products(g, m0, r0, min(rows, r0 + share), n0, threadIdx.x - 128,
+                            reinterpret_cast<float *>(base + g.direct));
         } else if (MODE == kProj && warp >= 4 && adapters) {
             const int tid = threadIdx.x - 128;
             list_adapters(s_ad, g, m0, 128, tid);
@@ -949,7 +988,6 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (MODE == kProj && append)
                 for (int q = 0; q < splits; ++q)
                     bad |= tc::ld_cluster(splits > 1 ? tc::map_rank(smem_u32(&s_ad.bad), q) : smem_u32(&s_ad.bad));
-            if (MODE == kProj && g.direct) pdl_wait();  // v
             constexpr int U = 4;
 #pragma unroll 1
             for (int i0 = threadIdx.x; i0 < (r1 - r0) * per_row; i0 += U * kSmallThreads) {
@@ -1004,7 +1042,11 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         store_bf16<4>(g.v + (size_t)m * g.rank + part * 128 + col[k] % lines, v[k]);
                         continue;
                     }
-                    if (MODE == kProj && g.direct) add_direct(g, m, n0 + col[k], v[k]);
+                    if (MODE == kProj && adapters && g.direct) {
+                        const float4 d = *reinterpret_cast<const float4 *>(
+                            base + g.direct + 4 * ((row[k] - r0) * g.width + col[k]));
+                        v[k][0] += d.x, v[k][1] += d.y, v[k][2] += d.z, v[k][3] += d.w;
+                    }
                     if (MODE == kProj && bad) add_left_out<4>(g, m, n0 + col[k], v[k]);
                     finish<MODE, ACT, 4>(g, m, half, n0 + col[k], v[k], u[k], side[k]);
                 }
@@ -1057,6 +1099,7 @@ struct Maps {
 
 constexpr int kMaxSplits = 8;  // portable cluster size
 constexpr size_t kSmallSmem = 200 * 1024;  // of one CTA's stages
+constexpr size_t kMaxDelta = 16 * 1024;    // of direct_products' outputs
 
 // Lines of A in a CTA's stage: 128; in the single-CTA kernel the rows there are
 // (8-line groups of the swizzle) where they are 64 or fewer.
@@ -1137,7 +1180,7 @@ template <int MODE, int ACT>
 cudaError_t small_attribute() {
     static PerDeviceOnce once;
     return per_device_once(once, [] {
-        return smem_attributes(small_kernel<MODE, ACT>, kSmallSmem + 1024);
+        return smem_attributes(small_kernel<MODE, ACT>, kSmallSmem + kMaxDelta + 1024);
     });
 }
 
@@ -1173,6 +1216,11 @@ cudaError_t cluster_fill(int num_sms, ClusterFill *out) {
     return e;
 }
 
+// Shared memory of the outputs that direct_products leaves.
+size_t delta_bytes(int M, const Plan &plan) {
+    return (size_t)ceil_div(M < 128 ? M : 128, plan.splits) * plan.width * 4;
+}
+
 // `beside`: the launch and one after it are to share the SMs (kInner and the
 // single-CTA projection).
 template <int MODE, int ACT>
@@ -1204,6 +1252,10 @@ cudaError_t launch_small(const Maps &m, GemmArgs g, const Plan &plan, int num_sm
     if (stages > kSmallMaxStages) stages = kSmallMaxStages;
     size_t smem = (size_t)(per * stages + extra) * stage + tail;
     if (smem < kParts) smem = kParts;
+    if (MODE == kProj && g.direct) {
+        g.direct = (int)smem;
+        smem += delta_bytes(g.M, plan);
+    }
     return launch_cluster(small_kernel<MODE, ACT>, (unsigned)ctas, kSmallThreads, smem + 1024,
                           plan.splits > 1 ? plan.splits : 0, s, m.a, m.b0, m.b1, g, stages, per, plan.splits, lines);
 }
@@ -1341,9 +1393,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         // Inner products by plain loads: x once per four ranks and A once per token
         // (2.5 T rank K bytes), or per up to four tokens of a run (1 to 2.5),
         // through L2 at about 6 TB/s, and 2 us for each time the SMs fill with
-        // CTAs; or by kInner, 6.5 us and 0.4 per K block.  v B^T as the rows are
-        // finished: 2 x width rank bytes per row of a CTA (16 per clock: every
-        // lane's load is a line of its own), against about 2 us of appended blocks.
+        // CTAs; or by kInner, 6.5 us and 0.4 per K block.
         const int mt = ceil_div(p.T, 128);
         int inner_splits = 1;
         while (inner_splits < kMaxSplits && 2 * mt * inner_splits <= num_sms && g.kb / (2 * inner_splits) >= 4)
@@ -1352,9 +1402,16 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         const double inner_us = ctas > 8 * num_sms
                                     ? 1.6 * p.T * (double)p.rank * p.K / 6e6 + 2.0 * ceil_div(ctas / 4, 4 * num_sms)
                                     : 2.5 * p.T * (double)p.rank * p.K / 6e6 + 2.0;
-        const double rows = (p.T < 128 ? p.T : 128) / (double)plan.splits;
-        const double add_us = rows * plan.width * 2 * p.rank / 16 / 1900;
-        g.direct = !plan.pairs && add_us < 2;
+        // v B^T by plain products: about 2.2 us for two groups of four outputs per
+        // thread and 16 ranks, part of it beside the K loop; or by appended
+        // blocks, 1.8 us each for the adapters that a tile may name (the tokens of
+        // a long batch are taken to come in runs).
+        const int rows = p.T < 128 ? p.T : 128;
+        const int items = ceil_div(rows, plan.splits) * (plan.width / 4);
+        const int distinct = p.T <= 64 ? (p.n < p.T ? p.n : p.T) : (p.n < 12 ? p.n : 12);
+        const int blocks = ceil_div(adapter_blocks(distinct, p.rank), plan.splits);
+        const double direct_us = 2.2 * ceil_div(items, 2 * kGroup) * ceil_div(p.rank, 16);
+        g.direct = !plan.pairs && delta_bytes(p.T, plan) <= kMaxDelta && direct_us < 0.3 * plan.us + 0.5 + 1.8 * blocks;
         const bool plain = !plan.pairs && inner_us < 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
         beside = !plan.pairs && !plain;
         if (plain) {
