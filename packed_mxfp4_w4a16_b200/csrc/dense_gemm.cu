@@ -507,7 +507,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     volatile int *abort = &s_abort;
     // With adapters this kernel follows kInner, which lets it start only
     // after its own inputs were complete: just v, which kInner writes, has to
-    // be waited for, and only by the warps that read it.
+    // be waited for.  Every warp does so before its first wait on a barrier
+    // that needs v: those waits are bounded, kInner's run is not.
     const bool adapters = MODE == kProj && g.n > 0, late = adapters || g.late;
     if (!late) pdl_wait();
     pdl_launch_dependents();
@@ -556,6 +557,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 }
                 __syncwarp();
             }
+            if (adapters && t == pair) pdl_wait();
         }
         // on the way out after a wait gave up: nothing of this CTA in flight
         // (the leader's barriers count both CTAs' bytes)
@@ -596,6 +598,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     any = true;
                 }
                 if (MODE == kProj && adapters) {
+                    if (t == pair) pdl_wait();
                     for (bool last = false; ok && !last; ++x) {
                         ok = __all_sync(0xffffffffu, tc::wait<true>(&s_xfull, x & 1, abort));
                         if (!ok) break;
@@ -666,6 +669,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         const uint32_t empty0 = tc::map_rank(smem_u32(&s_tempty[0]), 0);
         const uint32_t empty1 = tc::map_rank(smem_u32(&s_tempty[1]), 0);
         int j = 0;
+        if (adapters) pdl_wait();
 #pragma unroll 1
         for (int t = pair; t < tiles; t += pairs, ++j) {
             const int buf = j & 1;
@@ -887,6 +891,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 __syncwarp();
             }
             if (MODE == kProj && append) {
+                pdl_wait();
                 for (bool last = false; !last; ++x) {
                     ok = __all_sync(0xffffffffu, ok && tc::wait(&s_xfull, x & 1, abort));
                     if (!ok) break;
@@ -950,7 +955,9 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 if (e + 1 < e1) fetch_block(f, s_ad, g, e + 1, m0, 0, n0, g.width, tid, false);
             }
         }
-        // every warp: the sums are complete (so all copies have been used too)
+        // every warp: the sums are complete (so all copies have been used too);
+        // with appended blocks not before v is
+        if (append) pdl_wait();
         const bool ok = tc::wait(&s_done, round & 1, abort);
         if (__syncthreads_and(ok)) {
             tc::fence_after();
@@ -1152,7 +1159,7 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
     const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
     for (int l = 0; l < 4; ++l) {
         const int splits = 1 << l;
-        if (l > 0 && g.kb / splits < 4) break;
+        if (l > 0 && (g.kb / splits < 4 || fill.ctas[l] < splits)) break;
         const int64_t room = fill.ctas[l] / (mt * splits);  // tiles along N that run at once
         for (int narrow = 0; narrow < 2; ++narrow) {
             Plan p = {0, false, splits, most, 0, 0};
