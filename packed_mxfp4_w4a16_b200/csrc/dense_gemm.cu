@@ -10,6 +10,8 @@
 //   kProj  T x N    = x W^T + v B^T (+ residual): the adapters' inner products
 //          v and the rows of their B appended to K, one block of 64 at a time
 //   kInner v = scale (x A^T) for the adapters that a tile's tokens name
+//   kInnerAll the same as one product with every adapter's A, T x (n rank), of
+//          which each row keeps its own adapter's columns
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -22,7 +24,7 @@ namespace moe {
 
 namespace {
 
-enum Mode { kFwd, kBwd, kDx, kDw, kProj, kInner };
+enum Mode { kFwd, kBwd, kDx, kDw, kProj, kInner, kInnerAll };
 
 struct GemmArgs {
     const uint16_t *dh;        // kBwd
@@ -167,6 +169,15 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
         uint16_t *r = g.out0 + row * 2 * g.N + n;
         store_bf16<W>(r, o);
         store_bf16<W>(r + g.N, p);
+    } else if (MODE == kInnerAll) {
+        // these columns are of one adapter (its rank is a multiple of 8)
+        const int id = g.ids[row], a = n / g.rank;
+        if (id == a) {
+            const float sc = g.scale[id];
+#pragma unroll
+            for (int i = 0; i < W; ++i) o[i] = v[i] * sc;
+            store_bf16<W>(g.v + row * g.rank + (n - a * g.rank), o);
+        }
     } else if (MODE == kDw) {
         store_bf16<W>((half ? g.out1 : g.out0) + row * g.N + n, v);
     } else {
@@ -183,7 +194,7 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
 
 // ------------------------------------------------------------- adapters --
 // The tokens of one tile name some set of adapters.  A group of 128 threads
-// lists them (in order of their first token), and appends to the tile's K
+// lists them, and appends to the tile's K
 // loop blocks of 64 columns that hold several adapters side by side (64 /
 // rank of them, or 64 of one adapter's columns): the A operand holds a
 // token's v in the columns of its own adapter and zeros in the others', the B
@@ -198,7 +209,10 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
 struct __align__(16) AdapterSmem {
     int ids[256];    // of the tile's rows; -1: none
     int list[256];   // distinct ids
-    int first[256];
+    union {
+        int first[256];        // whether a row is the first of its adapter
+        unsigned named[32];    // pools of up to 1024: a bit per adapter
+    };
     int count;
     int cmd;         // to the MMA thread: 1 a block is in the buffer, 2 the tile's last
     int bad;         // a non-finite element of B was left out
@@ -219,8 +233,11 @@ __device__ __forceinline__ bool group_all(bool ok) {
 __device__ __forceinline__ void group_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kGroup) : "memory"); }
 
 // ids, list and count of rows m0 .. m0 + rows - 1 (rows 128 or 256; rows past
-// M have none); tid: index in the group.
+// M have none); tid: index in the group.  Pools of up to 1024 adapters are
+// listed by id from a bitmap, larger ones in the order of first rows.
 __device__ __forceinline__ void list_adapters(AdapterSmem &s, const GemmArgs &g, int m0, int rows, int tid) {
+    const bool bits = g.n <= 1024;
+    if (bits && tid < 32) s.named[tid] = 0;
     for (int i = tid; i < rows; i += kGroup) {
         int id = m0 + i < g.M ? g.ids[m0 + i] : -1;
         if (id < -1 || id >= g.n) {
@@ -230,6 +247,28 @@ __device__ __forceinline__ void list_adapters(AdapterSmem &s, const GemmArgs &g,
         s.ids[i] = id;
     }
     group_sync();
+    if (bits) {
+        for (int i = tid; i < rows; i += kGroup) {
+            const int id = s.ids[i];
+            // (one of a run of equal neighbours marks it)
+            if (id >= 0 && (i == 0 || s.ids[i - 1] != id)) atomicOr(&s.named[id >> 5], 1u << (id & 31));
+        }
+        group_sync();
+        if (tid < 32) {
+            unsigned w = s.named[tid];
+            const int mine = __popc(w);
+            int before = mine;  // inclusive prefix sum over the words
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, before, o);
+                if (tid >= o) before += v;
+            }
+            if (tid == 31) s.count = before;
+            for (int at = before - mine; w; w &= w - 1) s.list[at++] = tid * 32 + __ffs(w) - 1;
+        }
+        group_sync();
+        return;
+    }
     for (int i = tid; i < rows; i += kGroup) {
         // compared with every earlier row, four per load and no early way out
         // (the loads of a scan that may stop wait for one another: 3 us)
@@ -653,9 +692,9 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     if (blocks && append_block(f, xa, xb, 128, half_cols, tid)) {
                         s_ad.bad = 1;
                         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_bad), "r"(1) : "memory");
+                        asm volatile("fence.acq_rel.cluster;" ::: "memory");
                     }
                     if (tid == 0) s_ad.cmd = (blocks ? 1 : 0) | (e + 1 >= blocks ? 2 : 0);
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
                     group_sync();
                     if (tid == 0) tc::arrive_release_cluster(xfull);
                     if (e + 1 < blocks)
@@ -1280,7 +1319,7 @@ cudaError_t launch_big(const Maps &m, GemmArgs g, const Plan &plan, int num_sms,
     g.width = plan.width;
     g.cols = plan.cols;
     g.n_fast = g.nt < g.mt;
-    g.wide = g.N % 16 == 0 && ((uintptr_t)g.out0 | (uintptr_t)g.out1) % 32 == 0;
+    g.wide = MODE != kInnerAll && g.N % 16 == 0 && ((uintptr_t)g.out0 | (uintptr_t)g.out1) % 32 == 0;
     const int64_t tiles = (int64_t)g.mt * g.nt;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
@@ -1421,8 +1460,23 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.direct = !plan.pairs && delta_bytes(p.T, plan) <= kMaxDelta && direct_us < 0.3 * plan.us + 0.5 + 1.8 * blocks;
         const bool plain = !plan.pairs && inner_us < 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
         beside = !plan.pairs && !plain;
+        // Every adapter's A in one product (1.4 PFLOP/s, however the tokens name
+        // them), where that is not much more than kInner takes for runs (x once
+        // at 3.7 TB/s and 8 us; for tokens that name them at random it takes a
+        // pass over x for every 128 columns of a tile's adapters).
+        const double all_us = 2.0 * p.T * p.K * p.n * p.rank / 1.4e9 + 4;
+        const bool all = plan.pairs && (int64_t)p.n * p.rank <= 65536 && all_us < 1.5 * (2.0 * p.T * p.K / 3.7e6 + 8);
         if (plain) {
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
+        } else if (all) {
+            GemmArgs ga = g;
+            ga.N = p.n * p.rank;
+            Plan inner = make_plan(kInnerAll, ga, num_sms, fill);
+            if (!inner.pairs) inner = Plan{0, true, 1, 256, 256, ceil_div(ga.N, 256)};
+            if ((e = map_tokens(&m.a, p.x, p.T, p.K, true)) != cudaSuccess) return e;
+            if ((e = map_weight(&m.b0, p.a, ga.N, p.K, inner)) != cudaSuccess) return e;
+            m.b1 = m.b0;
+            if ((e = launch_big<kInnerAll, 0>(m, ga, inner, num_sms, s)) != cudaSuccess) return e;
         } else {
             const int lines = p.rank < 128 ? p.rank : 128;
             if ((e = map_tokens(&m.a, p.x, p.T, p.K, false)) != cudaSuccess) return e;

@@ -168,6 +168,43 @@ def test_adapter_proj_many_tokens(T, K, N, rank, n, runs):
     check_adapter({"x": d["x"], "w": d["w"], "residual": d["residual"]}, "plain")
 
 
+@pytest.mark.parametrize("T,K,N,rank,n,runs", [(1285, 344, 2056, 8, 1, True), (1300, 136, 2048, 40, 64, False),
+                                               (1290, 72, 2048, 16, 1024, False), (1290, 72, 2048, 8, 1032, False),
+                                               (2049, 200, 1800, 24, 100, True), (200, 72, 64, 8, 1024, False),
+                                               (200, 72, 64, 8, 1025, False)])
+def test_adapter_proj_large_pools(T, K, N, rank, n, runs):
+    """Long batches whose tiles name many adapters, and pools on both sides of
+    the size up to which a tile lists them from a bitmap."""
+    check_adapter(adapter_inputs(T, K, N, rank, n, runs, seed=T), f"y {T} {K} {N} {rank} {n}")
+
+
+@pytest.mark.parametrize("rank", [24, 136])
+def test_bad_adapter_in_a_long_batch(rank):
+    T, N = 1300, 2056
+    d = adapter_inputs(T, 136, N, rank, 5, False, seed=rank)
+    whole = {k: v.clone() for k, v in d.items()}
+    clean = moe.moe_adapter_proj(**d)
+    mine = d["adapter_ids"] == 1
+    touched = torch.zeros(N, dtype=torch.bool, device="cuda")
+    touched[[0, 300, N - 1]] = True
+    d["lora_b"][1, touched, rank - 1] = float("inf")
+    y = moe.moe_adapter_proj(**d)
+    assert torch.equal(y[~mine], clean[~mine]) and torch.equal(y[mine][:, ~touched], clean[mine][:, ~touched])
+    assert not torch.isfinite(y[mine][:, touched]).any()
+    d["lora_a"][1, 2, 9] = float("nan")
+    y = moe.moe_adapter_proj(**d)
+    assert torch.equal(y[~mine], clean[~mine]) and not torch.isfinite(y[mine]).any()
+    d["adapter_ids"][mine] = 5
+    y = moe.moe_adapter_proj(**d)
+    assert moe.moe_dense_status() == moe.DEVICE_BAD_ADAPTER_ID
+    # (not the bits of `clean`: without adapter 1 the others' ranks share their
+    # steps of 16 products with other zeros, which is another order of one FP32 sum)
+    want, bound = adapter64(whole["x"], whole["w"], whole["lora_a"], whole["lora_b"], whole["lora_scale"],
+                            whole["adapter_ids"], whole["residual"])
+    assert_within(y[~mine], want[~mine], bound[~mine], "others")
+    assert torch.equal(y[mine], moe.moe_adapter_proj(d["x"], d["w"], residual=d["residual"])[mine])
+
+
 @pytest.mark.parametrize("T", [1, 5, 8, 40, 200])
 def test_plain_projection(T):
     d = adapter_inputs(T, 520, 264, 8, 1, False, seed=T)
