@@ -302,21 +302,33 @@ __host__ __device__ __forceinline__ int adapter_blocks(int count, int rank) {
     return (count + per - 1) / per;
 }
 
-// The adapter (index in the list, or -1) and its rank column of chunk c (8
-// columns) of appended block e.
-__device__ __forceinline__ void chunk_of(int e, int c, int rank, int count, int &at, int &col) {
-    if (rank > 64) {
-        const int per = (rank + 63) / 64;
-        at = e / per;
-        col = (e % per) * 64 + c * 8;
-        if (col >= rank) at = -1;
-    } else {
-        const int per = 64 / rank, slot = c * 8 / rank;
-        at = e * per + slot;
-        col = c * 8 - slot * rank;
-        if (slot >= per || at >= count) at = -1;
+// Walks the chunks (8 columns) of appended block e: the adapter (index in the
+// list) and its rank column of each.  One division per block at most: found
+// chunk by chunk, the divisions by the rank took 2 us of a block's 5.
+struct ChunkWalk {
+    int at, col, end;  // end: the first list index that is not in the block
+    __device__ __forceinline__ ChunkWalk(int e, int rank, int count) {
+        if (rank > 64) {
+            const int per = (rank + 63) / 64;
+            at = e / per;
+            col = (e - at * per) * 64;
+            end = at + 1;
+        } else {
+            const int per = 64 / rank;
+            at = e * per;
+            col = 0;
+            end = min(at + per, count);
+        }
     }
-}
+    __device__ __forceinline__ bool in() const { return at < end; }
+    __device__ __forceinline__ void next(int rank) {
+        col += 8;
+        if (col >= rank) {
+            col = 0;
+            ++at;
+        }
+    }
+};
 
 // Bits of the non-finite elements (all exponent bits set) of two BF16.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
@@ -333,22 +345,25 @@ __device__ __forceinline__ void fetch_block(AppendRow &f, const AdapterSmem &s, 
                                             int row0, int n, int cols, int tid, bool first) {
     const int id = s.ids[row0 + tid];
     const bool in = tid < cols && n + tid < g.N;
+    ChunkWalk w(e, g.rank, s.count);
+    unsigned own = 0;  // chunks of the row's own adapter
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        int at, col;
-        chunk_of(e, c, g.rank, s.count, at, col);
+    for (int c = 0; c < 8; ++c, w.next(g.rank)) {
         f.b[c] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && in)
-            f.b[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)s.list[at] * g.N + n + tid) * g.rank + col));
+        if (w.in()) {
+            const int ad = s.list[w.at];
+            if (in) f.b[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)ad * g.N + n + tid) * g.rank + w.col));
+            own |= (unsigned)(ad == id) << c;
+        }
     }
     if (first) pdl_wait();
+    // (they follow one another, from the row's column `col` of v on)
+    const int skip = own ? __ffs(own) - 1 : 0, col = g.rank > 64 ? ChunkWalk(e, g.rank, s.count).col : 0;
+    const uint16_t *v = g.v + (size_t)(m + tid) * g.rank + col;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        int at, col;
-        chunk_of(e, c, g.rank, s.count, at, col);
         f.a[c] = make_uint4(0, 0, 0, 0);
-        if (at >= 0 && s.list[at] == id)
-            f.a[c] = *reinterpret_cast<const uint4 *>(g.v + (size_t)(m + tid) * g.rank + col);
+        if (own >> c & 1) f.a[c] = *reinterpret_cast<const uint4 *>(v + (c - skip) * 8);
     }
 }
 // Into the operand tiles at `a` (room for `lines` rows) and `b` (`cols`),
