@@ -1474,24 +1474,23 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         const double direct_us = 2.2 * ceil_div(items, 2 * kGroup) * ceil_div(p.rank, 16);
         g.direct = !plan.pairs && delta_bytes(p.T, plan) <= kMaxDelta && direct_us < 0.3 * plan.us + 0.5 + 1.8 * blocks;
         const bool plain = !plan.pairs && inner_us < 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
-        beside = !plan.pairs && !plain;
-        // Every adapter's A in one product (1.4 PFLOP/s, however the tokens name
-        // them), where that is not much more than kInner takes for runs (x once
-        // at 3.7 TB/s and 8 us; for tokens that name them at random it takes a
-        // pass over x for every 128 columns of a tile's adapters).
-        const double all_us = 2.0 * p.T * p.K * p.n * p.rank / 1.4e9 + 4;
-        const bool all = plan.pairs && (int64_t)p.n * p.rank <= 65536 && all_us < 1.5 * (2.0 * p.T * p.K / 3.7e6 + 8);
+        // Every adapter's A in one product (however the tokens name them), where
+        // that is not much more than kInner takes for tokens that come in runs;
+        // for tokens that name adapters at random kInner takes a pass over x for
+        // every 128 columns of a tile's adapters.
+        GemmArgs ga = g;
+        ga.N = p.n <= 65536 / p.rank ? p.n * p.rank : 0;
+        const Plan every = ga.N ? make_plan(kInnerAll, ga, num_sms, fill) : Plan{1e30};
+        const double list_us = plan.pairs ? 2.0 * p.T * p.K / 3.7e6 + 8 : 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
+        const bool all = !plain && every.us < 1.5 * list_us;
+        beside = !plan.pairs && !plain && !all;
         if (plain) {
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
         } else if (all) {
-            GemmArgs ga = g;
-            ga.N = p.n * p.rank;
-            Plan inner = make_plan(kInnerAll, ga, num_sms, fill);
-            if (!inner.pairs) inner = Plan{0, true, 1, 256, 256, ceil_div(ga.N, 256)};
-            if ((e = map_tokens(&m.a, p.x, p.T, p.K, true)) != cudaSuccess) return e;
-            if ((e = map_weight(&m.b0, p.a, ga.N, p.K, inner)) != cudaSuccess) return e;
+            if ((e = map_tokens(&m.a, p.x, p.T, p.K, every.pairs)) != cudaSuccess) return e;
+            if ((e = map_weight(&m.b0, p.a, ga.N, p.K, every)) != cudaSuccess) return e;
             m.b1 = m.b0;
-            if ((e = launch_big<kInnerAll, 0>(m, ga, inner, num_sms, s)) != cudaSuccess) return e;
+            if ((e = launch_gemm<kInnerAll, 0>(m, ga, every, num_sms, s)) != cudaSuccess) return e;
         } else {
             const int lines = p.rank < 128 ? p.rank : 128;
             if ((e = map_tokens(&m.a, p.x, p.T, p.K, false)) != cudaSuccess) return e;
