@@ -302,86 +302,72 @@ __host__ __device__ __forceinline__ int adapter_blocks(int count, int rank) {
     return (count + per - 1) / per;
 }
 
-// Walks the chunks (8 columns) of appended block e: the adapter (index in the
-// list) and its rank column of each.  One division per block at most: found
-// chunk by chunk, the divisions by the rank took 2 us of a block's 5.
-struct ChunkWalk {
-    int at, col, end;  // end: the first list index that is not in the block
-    __device__ __forceinline__ ChunkWalk(int e, int rank, int count) {
-        if (rank > 64) {
-            const int per = (rank + 63) / 64;
-            at = e / per;
-            col = (e - at * per) * 64;
-            end = at + 1;
-        } else {
-            const int per = 64 / rank;
-            at = e * per;
-            col = 0;
-            end = min(at + per, count);
-        }
+// The adapter (index in the list, or -1) and its rank column of chunk c (8
+// columns) of appended block e.
+__device__ __forceinline__ void chunk_of(int e, int c, int rank, int count, int &at, int &col) {
+    if (rank > 64) {
+        const int per = (rank + 63) / 64;
+        at = e / per;
+        col = (e - at * per) * 64 + c * 8;
+        if (col >= rank) at = -1;
+    } else {
+        const int per = 64 / rank, slot = c * 8 / rank;
+        at = e * per + slot;
+        col = c * 8 - slot * rank;
+        if (slot >= per || at >= count) at = -1;
     }
-    __device__ __forceinline__ bool in() const { return at < end; }
-    __device__ __forceinline__ void next(int rank) {
-        col += 8;
-        if (col >= rank) {
-            col = 0;
-            ++at;
-        }
-    }
-};
+}
 
 // Bits of the non-finite elements (all exponent bits set) of two BF16.
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
     return ((w & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// A thread's share of an appended block: row `tid` of the A operand (a token's
-// v) and of the B operand (an output's row of the adapters' B).  Fetched ahead
-// of the buffer being free; kInner is waited for before the first v is read.
-struct AppendRow {
+// A thread's share of an appended block: chunk tid % 8 of every 16th row of the
+// A operand (a token's v) and of the B operand (an output's row of the
+// adapters' B).  Eight threads read a row's 128 bytes, and each has one chunk
+// to find (a row per thread, 32 lines per load: T 400, rank 32, 16 adapters at
+// random in 30.4 us instead of 24.8).  Fetched ahead of the buffer being free;
+// kInner is waited for before the first v is read.
+struct AppendRows {
     uint4 a[8], b[8];
 };
-__device__ __forceinline__ void fetch_block(AppendRow &f, const AdapterSmem &s, const GemmArgs &g, int e, int m,
+__device__ __forceinline__ void fetch_block(AppendRows &f, const AdapterSmem &s, const GemmArgs &g, int e, int m,
                                             int row0, int n, int cols, int tid, bool first) {
-    const int id = s.ids[row0 + tid];
-    const bool in = tid < cols && n + tid < g.N;
-    ChunkWalk w(e, g.rank, s.count);
-    unsigned own = 0;  // chunks of the row's own adapter
+    int at, col;
+    chunk_of(e, tid & 7, g.rank, s.count, at, col);
+    const int id = at < 0 ? -2 : s.list[at], r = tid >> 3;
+    const uint16_t *b = g.lora_b + ((int64_t)id * g.N + n + r) * g.rank + col;
+    const int last = id < 0 ? 0 : min(cols, g.N - n);
 #pragma unroll
-    for (int c = 0; c < 8; ++c, w.next(g.rank)) {
-        f.b[c] = make_uint4(0, 0, 0, 0);
-        if (w.in()) {
-            const int ad = s.list[w.at];
-            if (in) f.b[c] = __ldg(reinterpret_cast<const uint4 *>(g.lora_b + ((size_t)ad * g.N + n + tid) * g.rank + w.col));
-            own |= (unsigned)(ad == id) << c;
-        }
+    for (int i = 0; i < 8; ++i) {
+        f.b[i] = make_uint4(0, 0, 0, 0);
+        if (r + 16 * i < last) f.b[i] = __ldg(reinterpret_cast<const uint4 *>(b + (int64_t)16 * i * g.rank));
     }
     if (first) pdl_wait();
-    // (they follow one another, from the row's column `col` of v on)
-    const int skip = own ? __ffs(own) - 1 : 0, col = g.rank > 64 ? ChunkWalk(e, g.rank, s.count).col : 0;
-    const uint16_t *v = g.v + (size_t)(m + tid) * g.rank + col;
+    const uint16_t *v = g.v + (int64_t)(m + r) * g.rank + col;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        f.a[c] = make_uint4(0, 0, 0, 0);
-        if (own >> c & 1) f.a[c] = *reinterpret_cast<const uint4 *>(v + (c - skip) * 8);
+    for (int i = 0; i < 8; ++i) {
+        f.a[i] = make_uint4(0, 0, 0, 0);
+        if (s.ids[row0 + r + 16 * i] == id) f.a[i] = *reinterpret_cast<const uint4 *>(v + (int64_t)16 * i * g.rank);
     }
 }
 // Into the operand tiles at `a` (room for `lines` rows) and `b` (`cols`),
 // K-major with the 128-byte swizzle: 16-byte chunk c of row r lies at r * 128
 // + 16 (c ^ (r & 7)).  True if a non-finite element of B was left out.
-__device__ __forceinline__ bool append_block(const AppendRow &f, uint8_t *a, uint8_t *b, int lines, int cols,
+__device__ __forceinline__ bool append_block(const AppendRows &f, uint8_t *a, uint8_t *b, int lines, int cols,
                                              int tid) {
     bool bad = false;
+    const int r = tid >> 3, off = r * 128 + 16 * ((tid ^ r) & 7);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const uint32_t x = non_finite(f.b[c].x), y = non_finite(f.b[c].y), z = non_finite(f.b[c].z),
-                       w = non_finite(f.b[c].w);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t x = non_finite(f.b[i].x), y = non_finite(f.b[i].y), z = non_finite(f.b[i].z),
+                       w = non_finite(f.b[i].w);
         bad |= (x | y | z | w) != 0;
-        const uint32_t off = tid * 128 + 16 * (c ^ (tid & 7));
-        if (tid < lines) *reinterpret_cast<uint4 *>(a + off) = f.a[c];
-        if (tid < cols)
-            *reinterpret_cast<uint4 *>(b + off) =
-                make_uint4(f.b[c].x & ~x, f.b[c].y & ~y, f.b[c].z & ~z, f.b[c].w & ~w);
+        if (r + 16 * i < lines) *reinterpret_cast<uint4 *>(a + off + i * 2048) = f.a[i];
+        if (r + 16 * i < cols)
+            *reinterpret_cast<uint4 *>(b + off + i * 2048) =
+                make_uint4(f.b[i].x & ~x, f.b[i].y & ~y, f.b[i].z & ~z, f.b[i].w & ~w);
     }
     tc::fence_async();  // before the tensor core reads them
     return bad;
@@ -695,7 +681,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 place(t, m, half, n);
                 list_adapters(s_ad, g, m, 256, tid);
                 const int blocks = adapter_blocks(s_ad.count, g.rank);
-                AppendRow f;
+                AppendRows f;
                 if (blocks)
                     fetch_block(f, s_ad, g, 0, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid, true);
 #pragma unroll 1
@@ -996,7 +982,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const int blocks = adapter_blocks(s_ad.count, g.rank);
             const int e0 = blocks * rank / splits, e1 = blocks * (rank + 1) / splits;
             uint8_t *xa = base + stages * per * stage;
-            AppendRow f;
+            AppendRows f;
             if (e0 < e1) fetch_block(f, s_ad, g, e0, m0, 0, n0, g.width, tid, true);
             int x = 0;
 #pragma unroll 1
