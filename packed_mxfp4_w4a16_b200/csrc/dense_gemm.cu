@@ -36,6 +36,7 @@ struct GemmArgs {
     int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
     int n_fast;                // consecutive tiles share M (else N)
     int wide;                  // outputs allow 32-byte stores
+    int tail;                  // big_kernel: the last tiles, done as two of half the columns
     int width, cols;           // small_kernel: output columns per tile, columns of its products
     // adapters (kProj with n > 0, kInner)
     const int32_t *ids;        // [M]
@@ -517,9 +518,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = tc::cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int tiles = g.mt * g.nt;
-    const int half_cols = g.cols / 2;  // lines of B in each CTA
-    const uint32_t bytes = 2 * tc::kBox + half_cols * 128;
+    // The last `tail` tiles are done as two of half the columns each.
+    const int whole = g.mt * g.nt - g.tail, tiles = whole + 2 * g.tail;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBigStages; ++i) {
@@ -553,8 +553,11 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
     if (!late) pdl_wait();
     pdl_launch_dependents();
 
-    // tile -> first row of the pair's tile, half (kDw), first output column
+    // tile -> first row of the pair's tile, half (kDw), first output column;
+    // lines of B in each CTA
     auto place = [&](int t, int &m, int &half, int &n) {
+        const int part = t >= whole ? (t - whole) & 1 : 0, split = t >= whole;
+        if (split) t = whole + ((t - whole) >> 1);
         // strips of up to 8 tiles along the shorter dimension: the tiles of one
         // moment form a block that shares operands in L2
         const int fast = g.n_fast ? g.nt : g.mt, slow = g.n_fast ? g.mt : g.nt;
@@ -566,7 +569,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         half = MODE == kDw && mt >= g.mt_half;
         if (half) mt -= g.mt_half;
         m = mt * 256;
-        n = nt * g.width;
+        n = nt * g.width + part * (g.width >> 1);
+        return g.cols >> (1 + split);
     };
 
     if (warp == 0) {
@@ -577,7 +581,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 #pragma unroll 1
         for (int t = pair; t < tiles && ok; t += pairs) {
             int m, half, n;
-            place(t, m, half, n);
+            const int half_cols = place(t, m, half, n);
+            const uint32_t bytes = 2 * tc::kBox + half_cols * 128;
             m += rank * 128;
             if (!gated(MODE)) n += rank * half_cols;
 #pragma unroll 1
@@ -592,7 +597,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     tc::arrive_tx_cluster(bar, bytes);
                     load_a<MODE, 2>(dst, &map_a, g, kb, m, half, 2, bar);
                     load_b<MODE, 2>(dst + 2 * tc::kBox, &map_b0, &map_b1, g, kb, n, rank, bar);
-                    if (b_mn(MODE) && half_cols > 64)
+                    if ((b_mn(MODE) || g.tail) && half_cols > 64)
                         load_b<MODE, 2>(dst + 3 * tc::kBox, &map_b0, &map_b1, g, kb, n + 64, rank, bar);
                 }
                 __syncwarp();
@@ -607,7 +612,6 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
-            const uint32_t id = tc::idesc(256, g.cols, a_mn(MODE), b_mn(MODE));
             const uint64_t a0 = tc::desc<a_mn(MODE)>(smem), b0 = tc::desc<b_mn(MODE)>(smem + 2 * tc::kBox);
             const bool issue = tc::elect();
             tc::Ring at;
@@ -615,6 +619,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             bool ok = true, any = false;
 #pragma unroll 1
             for (int t = pair; t < tiles && ok; t += pairs, ++j) {
+                const uint32_t id = tc::idesc(256, g.cols >> (t >= whole), a_mn(MODE), b_mn(MODE));
                 const int buf = j & 1;
                 if (j >= 2) {
                     ok = __all_sync(0xffffffffu, tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort));
@@ -678,7 +683,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 #pragma unroll 1
             for (int t = pair; t < tiles && ok; t += pairs) {
                 int m, half, n;
-                place(t, m, half, n);
+                const int half_cols = place(t, m, half, n);
                 list_adapters(s_ad, g, m, 256, tid);
                 const int blocks = adapter_blocks(s_ad.count, g.rank);
                 AppendRows f;
@@ -717,12 +722,12 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
             int m, half, n;
-            place(t, m, half, n);
+            const int half_cols = place(t, m, half, n), width = gated(MODE) ? half_cols : 2 * half_cols;
             m += rank * 128 + (warp & 3) * 32 + lane;
             const uint32_t acc = base + buf * 256;
             // gated: two warps share the rows, each finishes every other 16 columns
 #pragma unroll 1
-            for (int c = gated(MODE) && warp >= 8 ? 16 : 0; c < g.width && n + c < g.N; c += gated(MODE) ? 32 : 16) {
+            for (int c = gated(MODE) && warp >= 8 ? 16 : 0; c < width && n + c < g.N; c += gated(MODE) ? 32 : 16) {
                 uint32_t v[16], u[16];
                 tc::tmem_ld16(acc + c, v);
                 if (gated(MODE)) tc::tmem_ld16(acc + half_cols + c, u);
@@ -1166,6 +1171,7 @@ struct Plan {
     double us;
     bool pairs;
     int splits, width, cols, nt;
+    int tail;  // pairs: the tiles of the last wave that are halved
 };
 
 // Time of `ctas` CTAs that take `blocks` K blocks of `stage` bytes each, of
@@ -1193,7 +1199,20 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
         Plan p = {0, true, 1, gated(mode) ? cols / 2 : cols, cols, 0};
         p.nt = ceil_div(g.N, p.width);
         const int64_t tiles = (int64_t)ceil_div(g.M, 256) * halves * p.nt;
-        p.us = stream_us(2 * tiles, g.kb, 2.0 * tc::kBox + cols * 64, once, num_sms / 2 * 2);
+        const double stage = 2.0 * tc::kBox + cols * 64;
+        p.us = stream_us(2 * tiles, g.kb, stage, once, num_sms / 2 * 2);
+        // a last wave with work for half of the pairs at most is done as tiles of
+        // half the columns, which take three quarters of the time (their rows of
+        // A are the same).  Projection of T 8192, K 7168, N 2048 with adapters
+        // 193.7 us instead of 200.3, backward pass of T 2048, H 2048, I 1536 62.9
+        // instead of 64.8; many waves change by less than the noise.
+        const int pairs = num_sms / 2, last = (int)(tiles % pairs);
+        if (cols == 256 && tiles > pairs && last > 0 && 2 * last <= pairs) {
+            const double part = (double)last / tiles;
+            p.tail = last;
+            p.us = stream_us(2 * (tiles - last), g.kb, stage, once * (1 - part), 2 * pairs) +
+                   stream_us(4 * last, g.kb, stage - cols * 32, once * part, 2 * pairs);
+        }
         if (p.us < 0.97 * best.us) best = p;
     }
     const int64_t mt = (int64_t)ceil_div(g.M, 128) * halves;
@@ -1319,9 +1338,10 @@ cudaError_t launch_big(const Maps &m, GemmArgs g, const Plan &plan, int num_sms,
     g.nt = plan.nt;
     g.width = plan.width;
     g.cols = plan.cols;
+    g.tail = plan.tail;
     g.n_fast = g.nt < g.mt;
     g.wide = MODE != kInnerAll && g.N % 16 == 0 && ((uintptr_t)g.out0 | (uintptr_t)g.out1) % 32 == 0;
-    const int64_t tiles = (int64_t)g.mt * g.nt;
+    const int64_t tiles = (int64_t)g.mt * g.nt + g.tail;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     return launch_cluster(big_kernel<MODE, ACT>, 2 * pairs, big_threads(MODE), kBigSmem, 0, s, m.a, m.b0, m.b1, g);
 }
@@ -1333,7 +1353,7 @@ cudaError_t map_tokens(CUtensorMap *m, const uint16_t *x, int64_t rows, int64_t 
 
 // A weight [rows][cols] as K-major operand B: lines per box as the plan's kernel loads them.
 cudaError_t map_weight(CUtensorMap *m, const uint16_t *w, int64_t rows, int64_t cols, const Plan &plan) {
-    return tc::map_matrix(m, w, rows, cols, plan.pairs ? plan.cols / 2 : plan.width);
+    return tc::map_matrix(m, w, rows, cols, plan.pairs ? plan.cols / (plan.tail ? 4 : 2) : plan.width);
 }
 
 template <int MODE, int ACT>
