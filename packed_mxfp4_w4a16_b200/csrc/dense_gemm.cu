@@ -1,8 +1,8 @@
 // dense_gemm.cu — the dense feed-forward products on tcgen05 (FP32
 // accumulators in TMEM, operands brought in by TMA with the 128-byte swizzle).
 //
-// One kernel body serves the five products, which differ in where their
-// operands come from and in their epilogue (M x N = sum over K):
+// The products differ in where their operands come from and in their epilogue
+// (M x N = sum over K):
 //   kFwd   T x I    = x Wg^T and x Wu^T side by side; h = act(g) * u
 //   kBwd   the same sums; dg and du from them and dh
 //   kDx    T x H    = dg Wg + du Wu   (K runs over the halves of [dg | du])
@@ -195,8 +195,7 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
 
 // ------------------------------------------------------------- adapters --
 // The tokens of one tile name some set of adapters.  A group of 128 threads
-// lists them, and appends to the tile's K
-// loop blocks of 64 columns that hold several adapters side by side (64 /
+// lists them, and appends to the tile's K loop blocks of 64 columns that hold several adapters side by side (64 /
 // rank of them, or 64 of one adapter's columns): the A operand holds a
 // token's v in the columns of its own adapter and zeros in the others', the B
 // operand the adapters' B rows.  So one accumulator receives every token's
@@ -710,7 +709,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                     // in 406 us instead of 353.
                     if (tid == 0) tc::arrive_cluster(xfull);
                     if (e + 1 < blocks)
-                        fetch_block(f, s_ad, g, e + 1, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid, false);
+                        fetch_block(f, s_ad, g, e + 1, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid,
+                                    false);
                 }
                 group_sync();  // the list is rebuilt for the next tile
             }
