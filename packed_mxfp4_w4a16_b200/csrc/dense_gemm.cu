@@ -195,11 +195,11 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
 
 // ------------------------------------------------------------- adapters --
 // The tokens of one tile name some set of adapters.  A group of 128 threads
-// lists them, and appends to the tile's K loop blocks of 64 columns that hold several adapters side by side (64 /
-// rank of them, or 64 of one adapter's columns): the A operand holds a
-// token's v in the columns of its own adapter and zeros in the others', the B
-// operand the adapters' B rows.  So one accumulator receives every token's
-// own correction, for any mixture of adapters.
+// lists them, and appends to the tile's K loop blocks of 64 columns that hold
+// several adapters side by side (64 / rank of them, or 64 of one adapter's
+// columns): the A operand holds a token's v in the columns of its own adapter
+// and zeros in the others', the B operand the adapters' B rows.  So one
+// accumulator receives every token's own correction, for any mixture.
 //
 // Zeros do not hide infinities and NaN (0 * inf is NaN), and one request's
 // broken adapter must not reach another's tokens: non-finite elements of B

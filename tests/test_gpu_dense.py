@@ -150,6 +150,17 @@ def check_adapter(d, what, **kw):
     return y
 
 
+@pytest.mark.parametrize("T,H,I", [(2600, 1032, 2568), (5000, 1032, 520), (2561, 520, 1032)])
+def test_gated_last_wave_of_half_tiles(T, H, I):
+    """Few tiles over a whole number of waves, and columns that end inside a half tile."""
+    x, wg, wu = gated_inputs(T, H, I, seed=T)
+    assert_within(moe.moe_gated_ffn(x, wg, wu), *gated64(x, wg, wu, "silu"), "h")
+    dh = normal((T, I), 0.1, T + 5)
+    want, bound = gated_backward64(x, wg, wu, dh, "silu")
+    for got, w, b, name in zip(moe.moe_gated_ffn_backward(x, wg, wu, dh), want, bound, ("dx", "dwg", "dwu")):
+        assert_within(got, w, b, name)
+
+
 PROJ = [(8, 8, 8, 1), (136, 72, 24, 3), (384, 512, 16, 20), (1000, 520, 64, 7), (1536, 2048, 16, 40),
         (2048, 264, 40, 5), (264, 392, 136, 4), (512, 256, 256, 3)]
 
@@ -170,7 +181,8 @@ def test_adapter_proj_many_tokens(T, K, N, rank, n, runs):
 
 @pytest.mark.parametrize("T,K,N,rank,n,runs", [(1285, 344, 2056, 8, 1, True), (1300, 136, 2048, 40, 64, False),
                                                (1290, 72, 2048, 16, 1024, False), (1290, 72, 2048, 8, 1032, False),
-                                               (2049, 200, 1800, 24, 100, True), (200, 72, 64, 8, 1024, False),
+                                               (2049, 200, 1800, 24, 100, True), (2600, 72, 5368, 24, 5, False),
+                                               (2600, 72, 5160, 136, 3, True), (200, 72, 64, 8, 1024, False),
                                                (200, 72, 64, 8, 1025, False)])
 def test_adapter_proj_large_pools(T, K, N, rank, n, runs):
     """Long batches whose tiles name many adapters, and pools on both sides of
