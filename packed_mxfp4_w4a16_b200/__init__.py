@@ -374,20 +374,33 @@ def _is(t, dtype, shape):
     return t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
+def _other(stream, like):
+    """Whether `stream` is given and not the current one of the device of
+    `like`.  What a call allocates must then belong to `stream`: the allocator
+    hands memory of the current stream out again while that stream's last work
+    on it is still to come, and kernels on `stream` would not wait for it."""
+    return stream is not None and like.is_cuda and stream != torch.cuda.current_stream(like.device)
+
+
 def _new(like, shape, stream):
-    """A new BF16 output beside `like`, used on `stream`."""
-    t = torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    """A new BF16 output beside `like`, written on `stream`; the current stream
+    may read it too (ordered behind the call)."""
+    if _other(stream, like):
+        current = torch.cuda.current_stream(like.device)
+        with torch.cuda.stream(stream):
+            t = like.new_empty(shape)
+        t.record_stream(current)
+        return t
+    return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
 
 
 def _workspace(ws, need, like, name, stream):
     if ws is None:
-        ws = like.new_empty(need, dtype=torch.uint8)
-        if stream is not None:
-            ws.record_stream(stream)
-    elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        if _other(stream, like):
+            with torch.cuda.stream(stream):
+                return like.new_empty(need, dtype=torch.uint8)
+        return like.new_empty(need, dtype=torch.uint8)
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise MoEError(f"{name} (workspace)", -1)
     return ws
 
