@@ -178,6 +178,10 @@ __device__ __forceinline__ void finish(const GemmArgs &g, int64_t row, int half,
 #pragma unroll
             for (int i = 0; i < W; ++i) o[i] = v[i] * sc;
             store_bf16<W>(g.v + row * g.rank + (n - a * g.rank), o);
+        } else if (n == 0 && (id < -1 || id >= g.n)) {
+            // (once per row; the projection may take plain products, which
+            // pass over such ids)
+            atomicOr(g.status, kBadAdapterStatus);
         }
     } else if (MODE == kDw) {
         store_bf16<W>((half ? g.out1 : g.out0) + row * g.N + n, v);
