@@ -575,8 +575,11 @@ MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint1
                              void *workspace, size_t bytes, void *stream);
 
 /* Device status word of the dense calls on the current device (MOE_DEVICE_*
- * bits, accumulated since the last read): synchronises `stream`, copies the
- * word to *device_status and clears it.  Errors: ARG, UNSUPPORTED, CUDA. */
+ * bits, accumulated since the last read): synchronises `stream`, takes the
+ * word out and returns it in *device_status.  The word is shared by all
+ * streams and callers of the GPU.  A bit that a kernel sets during the read is
+ * returned by this read or by the next one, to whichever caller makes it.
+ * Errors: ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_dense_status(void *stream, unsigned *device_status);
 
 /* Human-readable name of a status code (static string, never NULL). */

@@ -4,14 +4,21 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "dense.cuh"
 #include "host_checks.cuh"
 
 namespace {
 
 // One status word per GPU that loads the library (as the scratch of
-// moe_forward_noalloc): the dense calls have no handle to keep one in.
+// moe_forward_noalloc): the dense calls have no handle to keep one in.  A line
+// further: what a read of it has taken out.
 __device__ unsigned g_dense_status[64];
+constexpr int kTaken = 32;
+
+// Kernels on any stream may set bits meanwhile: each is taken here or stays.
+__global__ void take_status_kernel(unsigned *status) { status[kTaken] = atomicExch(status, 0u); }
 
 struct DeviceInfo {
     int rc = MOE_ERR_CUDA;
@@ -242,9 +249,15 @@ int moe_dense_status(void *stream, unsigned *device_status) {
     if (rc != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned v = 0;
-    if (cudaStreamSynchronize(s) != cudaSuccess ||
-        cudaMemcpyAsync(&v, d.status, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemsetAsync(d.status, 0, sizeof v, s) != cudaSuccess ||
+    static std::mutex reading;  // one reader at a time has the taken word
+    std::lock_guard<std::mutex> lock(reading);
+    if (cudaStreamSynchronize(s) != cudaSuccess) {
+        cudaGetLastError();
+        return MOE_ERR_CUDA;
+    }
+    take_status_kernel<<<1, 1, 0, s>>>(d.status);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyAsync(&v, d.status + kTaken, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
