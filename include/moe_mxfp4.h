@@ -582,6 +582,12 @@ MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint1
  * Errors: ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_dense_status(void *stream, unsigned *device_status);
 
+/* Polls of each bounded in-kernel wait of the dense calls made from now on, in
+ * this process (default 2^22; a poll of a wait that nothing ends takes about
+ * 1.5 us).  A wait that runs out sets MOE_DEVICE_TIMEOUT; the outputs of that
+ * call are then invalid.  For tests.  Errors: ARG (negative). */
+MOE_API int moe_dense_set_spin_limit(int polls);
+
 /* Human-readable name of a status code (static string, never NULL). */
 MOE_API const char *moe_status_string(int status);
 

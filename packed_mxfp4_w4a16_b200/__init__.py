@@ -39,6 +39,7 @@ __all__ = [
     "DEVICE_BAD_EXPERT_ID",
     "moe_gated_ffn", "moe_gated_ffn_backward_workspace_bytes", "moe_gated_ffn_backward",
     "moe_adapter_proj_workspace_bytes", "moe_adapter_proj", "moe_dense_status",
+    "moe_dense_set_spin_limit",
     "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FFN_RMSNORM", "DEVICE_BAD_ADAPTER_ID",
 ]
 
@@ -553,6 +554,11 @@ def moe_dense_status(stream=None) -> int:
     v = C.c_uint()
     check("moe_dense_status", load().moe_dense_status(_s(stream), C.byref(v)))
     return v.value
+
+
+def moe_dense_set_spin_limit(polls: int) -> None:
+    """Polls of each bounded wait of later dense calls (default 2^22)."""
+    check("moe_dense_set_spin_limit", load().moe_dense_set_spin_limit(polls))
 
 
 # ------------------------------------------------------------- bundles

@@ -62,6 +62,7 @@ SIGNATURES = [
     ("moe_adapter_proj", _i, [_vp, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                               _vp]),
     ("moe_dense_status", _i, [_vp, C.POINTER(_u)]),
+    ("moe_dense_set_spin_limit", _i, [_i]),
 ]
 
 

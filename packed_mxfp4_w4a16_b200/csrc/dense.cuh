@@ -11,6 +11,10 @@ namespace moe {
 
 constexpr unsigned kBadAdapterStatus = 0x4u;  // MOE_DEVICE_BAD_ADAPTER_ID
 
+// Polls of a wait before it gives up (about 6 s).  An accumulator is waited for
+// over a whole K loop, so the bound is longer than a copy's.
+constexpr int kDensePolls = 1 << 22;
+
 struct GatedParams {
     const uint16_t *x;       // [T][H]
     const uint16_t *wg, *wu; // [I][H]
@@ -20,6 +24,7 @@ struct GatedParams {
     uint16_t *dx;            // [T][H] or null
     uint16_t *dwg, *dwu;     // [I][H] or both null
     unsigned *status;
+    int polls;               // of a bounded wait
     int T, H, I, act;
 };
 
@@ -34,6 +39,7 @@ struct AdapterParams {
     uint16_t *y;               // [T][N]
     float *v;                  // workspace
     unsigned *status;
+    int polls;                 // of a bounded wait
     int T, K, N, n, rank;
 };
 

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "dense.cuh"
@@ -19,6 +20,8 @@ constexpr int kTaken = 32;
 
 // Kernels on any stream may set bits meanwhile: each is taken here or stays.
 __global__ void take_status_kernel(unsigned *status) { status[kTaken] = atomicExch(status, 0u); }
+
+std::atomic<int> g_polls{moe::kDensePolls};
 
 struct DeviceInfo {
     int rc = MOE_ERR_CUDA;
@@ -115,6 +118,7 @@ int moe_gated_ffn(const uint16_t *x, int T, int H, int I, const uint16_t *w_gate
     p.wu = w_up;
     p.h = h;
     p.status = d.status;
+    p.polls = g_polls.load(std::memory_order_relaxed);
     p.T = T;
     p.H = H;
     p.I = I;
@@ -173,6 +177,7 @@ int moe_gated_ffn_backward(const uint16_t *x, int T, int H, int I, const uint16_
     p.dwg = dw_gate;
     p.dwu = dw_up;
     p.status = d.status;
+    p.polls = g_polls.load(std::memory_order_relaxed);
     p.T = T;
     p.H = H;
     p.I = I;
@@ -233,6 +238,7 @@ int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint16_t *w,
     p.y = y;
     p.v = static_cast<float *>(workspace);
     p.status = d.status;
+    p.polls = g_polls.load(std::memory_order_relaxed);
     p.T = T;
     p.K = K;
     p.N = N;
@@ -263,6 +269,12 @@ int moe_dense_status(void *stream, unsigned *device_status) {
         return MOE_ERR_CUDA;
     }
     *device_status = v;
+    return MOE_OK;
+}
+
+int moe_dense_set_spin_limit(int polls) {
+    if (polls < 0) return MOE_ERR_ARG;
+    g_polls.store(polls, std::memory_order_relaxed);
     return MOE_OK;
 }
 

@@ -31,6 +31,7 @@ struct GemmArgs {
     const uint16_t *residual;  // kProj, or null
     uint16_t *out0, *out1;     // kDw: dWg, dWu; else out0
     unsigned *status;
+    int polls;                 // of a bounded wait
     int M, N;                  // rows of the output (kDw: of one half), its columns
     int kb, kb_half;           // K blocks of 64; kDx: of one half
     int mt, nt, mt_half;       // tiles along M and N; kDw: along M of one half
@@ -591,7 +592,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 #pragma unroll 1
             for (int kb = 0; kb < g.kb; ++kb, at.next(kBigStages)) {
                 if (at.pass > 0) {
-                    ok = tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort);
+                    ok = tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort, g.polls);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
@@ -607,11 +608,14 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
             }
             if (adapters && t == pair) pdl_wait();
         }
-        // on the way out after a wait gave up: nothing of this CTA in flight
-        // (the leader's barriers count both CTAs' bytes)
-        if (!ok && rank == 0)
-            for (uint32_t i = 0; i < (uint32_t)kBigStages; ++i)
-                if (at.pass > 0 || i < at.slot) mbar_wait(&s_full[i], (i < at.slot ? at.pass : at.pass - 1) & 1);
+        // Nothing in flight on the way out: once the products have used this
+        // CTA's last block, every copy of the pair up to it has landed.  (After a
+        // wait that gave up they may never: then the bound of this wait, 1.5 s,
+        // is the time in which they land.)
+        if (at.pass > 0 || at.slot > 0) {
+            at.prev(kBigStages);
+            mbar_wait(&s_empty[at.slot], at.pass & 1);
+        }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
@@ -625,13 +629,13 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 const uint32_t id = tc::idesc(256, g.cols >> (t >= whole), a_mn(MODE), b_mn(MODE));
                 const int buf = j & 1;
                 if (j >= 2) {
-                    ok = __all_sync(0xffffffffu, tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort));
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_tempty[buf], ((j >> 1) - 1) & 1, abort, g.polls));
                     if (!ok) break;
                 }
                 tc::fence_after();
 #pragma unroll 1
                 for (int kb = 0; kb < g.kb; ++kb, at.next(kBigStages)) {
-                    ok = __all_sync(0xffffffffu, tc::wait(&s_full[at.slot], at.pass & 1, abort));
+                    ok = __all_sync(0xffffffffu, tc::wait(&s_full[at.slot], at.pass & 1, abort, g.polls));
                     if (!ok) break;
                     tc::fence_after();
                     const uint64_t da = a0 + at.slot * (kBigStage >> 4), db = b0 + at.slot * (kBigStage >> 4);
@@ -648,7 +652,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 if (MODE == kProj && adapters) {
                     if (t == pair) pdl_wait();
                     for (bool last = false; ok && !last; ++x) {
-                        ok = __all_sync(0xffffffffu, tc::wait<true>(&s_xfull, x & 1, abort));
+                        ok = __all_sync(0xffffffffu, tc::wait<true>(&s_xfull, x & 1, abort, g.polls));
                         if (!ok) break;
                         tc::fence_after();
                         const int cmd = *(volatile int *)&s_ad.cmd;
@@ -667,12 +671,16 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 if (ok && issue) tc::commit<2>(&s_tfull[buf]);
                 __syncwarp();
             }
-            // leaving early: the products issued so far have finished
-            if (!ok && any) {
-                const uint32_t last = at.slot ? at.slot - 1 : kBigStages - 1;
-                mbar_wait(&s_empty[last], (at.slot ? at.pass : at.pass - 1) & 1);
+            // the products issued so far have finished, whichever wait gave up
+            if (ok) {
+                if (j > 0) mbar_wait(&s_tfull[(j - 1) & 1], ((j - 1) >> 1) & 1);
+            } else {
+                if (any) {
+                    at.prev(kBigStages);
+                    mbar_wait(&s_empty[at.slot], at.pass & 1);
+                }
+                if (x > 0) mbar_wait(&s_xempty, (x - 1) & 1);
             }
-            if (!ok && x > 0) mbar_wait(&s_xempty, (x - 1) & 1);
         }
         __syncwarp();
     } else if (MODE == kProj && warp >= 8) {
@@ -695,7 +703,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 #pragma unroll 1
                 for (int e = 0; e < (blocks ? blocks : 1); ++e, ++x) {
                     if (x > 0) {
-                        ok = group_all(tc::wait(&s_xempty, (x - 1) & 1, abort));  // the whole group goes on or leaves
+                        ok = group_all(tc::wait(&s_xempty, (x - 1) & 1, abort, g.polls));  // the whole group goes on or leaves
                         if (!ok) break;
                     }
                     if (blocks && append_block(f, xa, xb, 128, half_cols, tid)) {
@@ -728,7 +736,7 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
 #pragma unroll 1
         for (int t = pair; t < tiles; t += pairs, ++j) {
             const int buf = j & 1;
-            const bool ok = tc::wait(&s_tfull[buf], (j >> 1) & 1, abort);
+            const bool ok = tc::wait(&s_tfull[buf], (j >> 1) & 1, abort, g.polls);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc::fence_after();
             int m, half, n;
@@ -865,11 +873,13 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     }
     tc::Ring at;
     int round = 0;
+    uint32_t issued = 0;  // stages of this round, in the lane that issues the copies
 #pragma unroll 1
     for (int w = w0; w < w1; w += wstep, ++round) {
         const int part = MODE == kInner ? w % g.parts : 0;
         const int a0 = MODE == kInner ? w / g.parts * g.per_tile : 0;
         const int slots = MODE == kInner ? min(g.per_tile, s_ad.count - a0) : 0;
+        issued = 0;
         if (warp == 0) {
             // (rows that the products read beyond a_lines are garbage that stays in
             // its rows)
@@ -878,12 +888,11 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                                                                                   : g.width * 128);
             const bool issue = tc::elect();
             bool ok = !*abort;
-            uint32_t issued = 0;
             // (a lane whose wait gives up goes on without issuing: the warp's
             // lanes keep the same way through the loop without a vote)
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; kb += per, at.next(stages)) {
-                if (at.pass > 0) ok = ok && tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort);
+                if (at.pass > 0) ok = ok && tc::wait(&s_empty[at.slot], (at.pass - 1) & 1, abort, g.polls);
                 if (issue && ok) {
                     const uint32_t bar = smem_u32(&s_full[at.slot]);
                     uint32_t dst = smem + at.slot * per * stage;
@@ -910,15 +919,6 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
                 __syncwarp();
             }
-            if (issue && !ok) {  // nothing in flight on the way out
-                const uint32_t total = (uint32_t)(kb1 - kb0 + per - 1) / per;
-                tc::Ring back = at;  // to the slot behind the last one issued
-                for (uint32_t i = issued; i < total; ++i) back.prev(stages);
-                for (uint32_t i = 0; i < min(issued, (uint32_t)stages); ++i) {
-                    back.prev(stages);
-                    mbar_wait(&s_full[back.slot], back.pass & 1);
-                }
-            }
             __syncwarp();
         } else if (warp == 1) {
             const uint32_t id = tc::idesc(128, g.cols, a_mn(MODE), b_mn(MODE));
@@ -928,7 +928,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             int x = 0;
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; kb += per, at.next(stages)) {
-                ok = ok && tc::wait(&s_full[at.slot], at.pass & 1, abort);
+                ok = ok && tc::wait(&s_full[at.slot], at.pass & 1, abort, g.polls);
                 tc::fence_after();
                 const uint64_t da = da0 + at.slot * per * (stage >> 4), db = db0 + at.slot * per * (stage >> 4);
                 if (issue && ok) {
@@ -948,7 +948,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (MODE == kProj && append) {
                 pdl_wait();
                 for (bool last = false; !last; ++x) {
-                    ok = __all_sync(0xffffffffu, ok && tc::wait(&s_xfull, x & 1, abort));
+                    ok = __all_sync(0xffffffffu, ok && tc::wait(&s_xfull, x & 1, abort, g.polls));
                     if (!ok) break;
                     tc::fence_after();
                     const int cmd = *(volatile int *)&s_ad.cmd;
@@ -965,7 +965,6 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
             if (issue) tc::commit<1>(&s_done);
             __syncwarp();
-            if (!ok) mbar_wait(&s_done, round & 1);
         } else if ((MODE == kBwd || MODE == kProj) && warp == 3) {
             // dh or the residual of the rows that this CTA finishes, into L2
             const uint16_t *side = MODE == kBwd ? g.dh : g.residual;
@@ -1002,7 +1001,7 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             int x = 0;
 #pragma unroll 1
             for (int e = e0; e < max(e1, e0 + 1); ++e, ++x) {
-                if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort))) break;
+                if (x > 0 && !group_all(tc::wait(&s_xempty, (x - 1) & 1, abort, g.polls))) break;
                 if (e < e1 && append_block(f, xa, xa + b_at, a_lines, g.width, tid)) s_ad.bad = 1;
                 if (tid == 0) s_ad.cmd = (e < e1 ? 1 : 0) | (e + 1 >= e1 ? 2 : 0);
                 group_sync();
@@ -1013,8 +1012,8 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // every warp: the sums are complete (so all copies have been used too);
         // with appended blocks not before v is
         if (append) pdl_wait();
-        const bool ok = tc::wait(&s_done, round & 1, abort);
-        if (__syncthreads_and(ok)) {
+        const bool ok = tc::wait(&s_done, round & 1, abort, g.polls);
+        if (__syncthreads_and(ok && !*abort)) {
             tc::fence_after();
             // TMEM -> shared memory: warp w takes lanes 32 (w % 4) .., every other
             // 16 columns
@@ -1032,7 +1031,19 @@ small_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         *reinterpret_cast<uint4 *>(parts + r * kPartPitch + c + q) =
                             make_uint4(v[q], v[q + 1], v[q + 2], v[q + 3]);
                 }
+        } else if (warp == 0) {
+            // some warp's wait gave up: nothing stays in flight, neither copies ...
+            const uint32_t total = (uint32_t)(kb1 - kb0 + per - 1) / per;
+            tc::Ring back = at;  // to the slot behind the last one issued
+            for (uint32_t i = issued; i < total; ++i) back.prev(stages);
+            for (uint32_t i = 0; i < min(issued, (uint32_t)stages); ++i) {
+                back.prev(stages);
+                mbar_wait(&s_full[back.slot], back.pass & 1);
+            }
+        } else if (warp == 1) {
+            mbar_wait(&s_done, round & 1);  // ... nor products
         }
+        __syncwarp();
         tc::fence_before();
         if (splits > 1)
             tc::cluster_sync();
@@ -1388,6 +1399,7 @@ cudaError_t launch_gated_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
+    g.polls = p.polls;
     g.M = p.T;
     g.N = p.I;
     g.kb = ceil_div(p.H, 64);
@@ -1412,6 +1424,7 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
+    g.polls = p.polls;
     g.M = p.T;
     g.N = p.H;
     g.kb_half = ceil_div(p.I, 64);
@@ -1437,6 +1450,7 @@ cudaError_t launch_dw_tc(const GatedParams &p, bool after_dx, int num_sms, cudaS
     m.b1 = m.b0;
     GemmArgs g = {};
     g.status = p.status;
+    g.polls = p.polls;
     g.M = p.I;
     g.N = p.H;
     g.kb = ceil_div(p.T, 64);
@@ -1452,6 +1466,7 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     if (e != cudaSuccess) return e;
     GemmArgs g = {};
     g.status = p.status;
+    g.polls = p.polls;
     g.M = p.T;
     g.N = p.N;
     g.kb = ceil_div(p.K, 64);

@@ -46,6 +46,7 @@ struct GemvArgs {
     const float *v;            // proj: [T][rank]
     const int32_t *ids;        // proj
     unsigned *status;
+    int polls;                 // of a bounded wait
     int T, K, rows, n, rank;
     int ring, chunk;           // ring slots, K elements in each
 };
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
             for (int c = 0; c < chunks; ++c, ++it) {
                 const int s = it % p.ring;
                 if (it >= p.ring) {
-                    ok = tc::wait(&s_empty[s], (it / p.ring - 1) & 1, abort);
+                    ok = tc::wait(&s_empty[s], (it / p.ring - 1) & 1, abort, p.polls);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                 }
@@ -135,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
                 if (row) bulk_load(ring0 + s * slot + lane * pitch, row + c * p.chunk, bytes, &s_full[s]);
             }
         }
-        if (!ok)  // nothing in flight on the way out
-            for (int j = it > p.ring ? it - p.ring : 0; j < it; ++j) mbar_wait(&s_full[j % p.ring], (j / p.ring) & 1);
+        // nothing in flight on the way out, whichever warp's wait gave up
+        for (int j = it > p.ring ? it - p.ring : 0; j < it; ++j) mbar_wait(&s_full[j % p.ring], (j / p.ring) & 1);
     } else {
         // the tokens, zero-padded to a multiple of 64 elements
         const int per_row = (int)((xp - 16) / 16);
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c, ++it) {
                 const int s = it % p.ring;
-                ok = ok && tc::wait(&s_full[s], (it / p.ring) & 1, abort);
+                ok = ok && tc::wait(&s_full[s], (it / p.ring) & 1, abort, p.polls);
 #pragma unroll 2
                 for (int sub = 0; sub < share; sub += 64) {
                     const int kc = warp * share + sub + q * 16;  // this thread's 16 elements
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_kernel(const GemvArgs p) {
                     mma_bf16(acc, a1.z, b1.z, a1.w, b1.w, x1.z, x1.w);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s_empty[s]);
+                // (after a wait that gave up the slot may still be filled: not handed on)
+                if (lane == 0 && ok) mbar_arrive(&s_empty[s]);
             }
             // rows g, g + 8 x tokens 2 q, 2 q + 1 of this warp's share of K
             float *mine = red + (buf * kWarps + warp) * 128;
@@ -377,6 +379,7 @@ cudaError_t launch_gated_gemv(const GatedParams &p, int num_sms, cudaStream_t s)
     g.w1 = p.wu;
     g.out = p.h;
     g.status = p.status;
+    g.polls = p.polls;
     g.T = p.T;
     g.K = p.H;
     g.rows = p.I;
@@ -410,6 +413,7 @@ cudaError_t launch_proj_gemv(const AdapterParams &p, int num_sms, cudaStream_t s
     g.v = p.v;
     g.ids = p.ids;
     g.status = p.status;
+    g.polls = p.polls;
     g.T = p.T;
     g.K = p.K;
     g.rows = p.N;

@@ -206,16 +206,15 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// Bounded wait on phase `parity` of *bar; gives up as well once *abort is
-// set, and sets it when it runs out.  kDenseSpin: an accumulator is waited
-// for over a whole K loop, so the bound is longer than a copy's.
+// Bounded wait on phase `parity` of *bar; gives up after `polls` polls (1.5 us
+// each when nothing comes) or once *abort is set, which it sets when it runs
+// out.
 // CLUSTER: acquire what the other CTA's threads wrote (costs about 0.1 us
 // more per wait; copies and tensor-core work need none of it).
-constexpr int kDenseSpin = 1 << 22;
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, int polls) {
 #pragma unroll 1
-    for (int i = 0; i < kDenseSpin; ++i) {
+    for (int i = 0; i < polls; ++i) {
         if (CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
