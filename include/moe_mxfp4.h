@@ -574,6 +574,22 @@ MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint1
                              const float *lora_scale, const int32_t *adapter_ids, uint16_t *y,
                              void *workspace, size_t bytes, void *stream);
 
+/* Which kernels a moe_adapter_proj call of these sizes (T >= 1) launches, for
+ * tests and tuning; nothing is launched.  plan: int[6] on the host:
+ *   [0] products x W^T: 0 streamed weights (few tokens), 1 tiles of single
+ *       CTAs, 2 tiles of CTA pairs
+ *   [1] CTAs (a cluster) that split their K
+ *   [2] inner products A x: 0 none, 1 plain loads, 2 tiles of the adapters that
+ *       a row tile names, 3 one product with every adapter's A
+ *   [3] CTAs (a cluster) that split their K (0 with no adapters)
+ *   [4] products with B: 1 plain, 0 as columns appended to K (or none)
+ *   [5] with [2] = 2: clusters that share a row tile's adapters, else 0
+ * num_sms 0 and cluster_ctas NULL: on the current device.  Otherwise on a GPU
+ * of num_sms SMs that runs cluster_ctas[0 .. 2] CTAs at once in clusters of 2, 4
+ * and 8 (a host without a GPU will do).  Errors: ARG, UNSUPPORTED, CUDA. */
+MOE_API int moe_adapter_proj_plan(int T, int K, int N, int n_adapters, int rank, int num_sms,
+                                  const int *cluster_ctas, int *plan);
+
 /* Device status word of the dense calls on the current device (MOE_DEVICE_*
  * bits, accumulated since the last read): synchronises `stream`, takes the
  * word out and returns it in *device_status.  The word is shared by all

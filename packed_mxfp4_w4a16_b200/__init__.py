@@ -38,7 +38,7 @@ __all__ = [
     "FUSION_NONE", "FUSION_ROUTER", "FUSION_LAYER", "moe_set_fusion",
     "DEVICE_BAD_EXPERT_ID",
     "moe_gated_ffn", "moe_gated_ffn_backward_workspace_bytes", "moe_gated_ffn_backward",
-    "moe_adapter_proj_workspace_bytes", "moe_adapter_proj", "moe_dense_status",
+    "moe_adapter_proj_workspace_bytes", "moe_adapter_proj", "moe_adapter_proj_plan", "moe_dense_status",
     "moe_dense_set_spin_limit",
     "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "FFN_RMSNORM", "DEVICE_BAD_ADAPTER_ID",
 ]
@@ -546,6 +546,18 @@ def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_id
         x.data_ptr(), T, K, N, w.data_ptr(), _ptr(residual), n, rank, pa, pb, ps, pi, y.data_ptr(),
         pw, need, _raw_stream(stream, x)))
     return y
+
+
+def moe_adapter_proj_plan(T, K, N, n_adapters=0, rank=0, num_sms=0, cluster_ctas=None) -> dict:
+    """Which kernels a moe_adapter_proj call of these sizes launches, on the
+    current device or on one of ``num_sms`` SMs that runs ``cluster_ctas`` =
+    (CTAs at once in clusters of 2, of 4, of 8)."""
+    plan = (C.c_int * 6)()
+    ctas = None if cluster_ctas is None else (C.c_int * 3)(*cluster_ctas)
+    check("moe_adapter_proj_plan", load().moe_adapter_proj_plan(T, K, N, n_adapters, rank, num_sms, ctas, plan))
+    return {"products": ("streamed", "single", "pairs")[plan[0]], "splits": plan[1],
+            "inner": ("none", "loads", "named", "every")[plan[2]], "inner_splits": plan[3],
+            "direct": bool(plan[4]), "groups": plan[5]}
 
 
 def moe_dense_status(stream=None) -> int:

@@ -61,6 +61,7 @@ SIGNATURES = [
     ("moe_adapter_proj_workspace_bytes", _i, [_i, _i, _i, _i, _i, C.POINTER(_sz)]),
     ("moe_adapter_proj", _i, [_vp, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                               _vp]),
+    ("moe_adapter_proj_plan", _i, [_i, _i, _i, _i, _i, _i, C.POINTER(_i), C.POINTER(_i)]),
     ("moe_dense_status", _i, [_vp, C.POINTER(_u)]),
     ("moe_dense_set_spin_limit", _i, [_i]),
 ]

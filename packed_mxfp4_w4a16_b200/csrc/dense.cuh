@@ -57,6 +57,14 @@ cudaError_t launch_dx_tc(const GatedParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_dw_tc(const GatedParams &p, bool after_dx, int num_sms, cudaStream_t s);
 cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s);
 
+// What a projection of these sizes takes (see moe_adapter_proj_plan);
+// cluster_ctas: [3], or null for the current device's.
+struct AdapterPlan {
+    int products, splits, inner, inner_splits, direct, groups;
+};
+cudaError_t adapter_plan(int T, int K, int N, int n, int rank, int num_sms, const int *cluster_ctas,
+                         AdapterPlan *out);
+
 size_t adapter_workspace(int T, int K, int N, int n, int rank);
 cudaError_t launch_adapter_proj(const AdapterParams &p, int num_sms, cudaStream_t s);
 

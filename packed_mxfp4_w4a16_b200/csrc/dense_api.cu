@@ -247,6 +247,26 @@ int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint16_t *w,
     return moe::cuda_rc(moe::launch_adapter_proj(p, d.sms, static_cast<cudaStream_t>(stream)));
 }
 
+int moe_adapter_proj_plan(int T, int K, int N, int n_adapters, int rank, int num_sms,
+                          const int *cluster_ctas, int *plan) {
+    size_t need = 0;
+    int rc = moe_adapter_proj_workspace_bytes(T, K, N, n_adapters, rank, &need);
+    if (rc != MOE_OK) return rc;
+    if (!plan || T == 0 || num_sms < 0 || (num_sms > 0) != (cluster_ctas != nullptr)) return MOE_ERR_ARG;
+    if (num_sms == 0) {
+        int dev = 0;
+        DeviceInfo d;
+        if ((rc = device_info(&dev, &d)) != MOE_OK) return rc;
+        num_sms = d.sms;
+    }
+    moe::AdapterPlan p;
+    if ((rc = moe::cuda_rc(moe::adapter_plan(T, K, N, n_adapters, rank, num_sms, cluster_ctas, &p))) != MOE_OK)
+        return rc;
+    const int v[6] = {p.products, p.splits, p.inner, p.inner_splits, p.direct, p.groups};
+    for (int i = 0; i < 6; ++i) plan[i] = v[i];
+    return MOE_OK;
+}
+
 int moe_dense_status(void *stream, unsigned *device_status) {
     if (!device_status) return MOE_ERR_ARG;
     int dev = 0;

@@ -1216,7 +1216,7 @@ Plan make_plan(int mode, const GemmArgs &g, int num_sms, const ClusterFill &fill
     Plan best = {1e30, true, 1, 0, 0, 0};
     // narrower pair tiles only where every wave is full of work: a block's
     // products and its loads shrink with the columns, its rows of A do not
-    for (int cols = 256; g.M > 128 && cols >= 128; cols -= b_mn(mode) ? 128 : 32) {
+    for (int cols = 256; g.M > 128 && fill.ctas[1] >= 2 && cols >= 128; cols -= b_mn(mode) ? 128 : 32) {
         Plan p = {0, true, 1, gated(mode) ? cols / 2 : cols, cols, 0};
         p.nt = ceil_div(g.N, p.width);
         const int64_t tiles = (int64_t)ceil_div(g.M, 256) * halves * p.nt;
@@ -1306,6 +1306,93 @@ cudaError_t cluster_fill(int num_sms, ClusterFill *out) {
 // Shared memory of the outputs that direct_products leaves.
 size_t delta_bytes(int M, const Plan &plan) {
     return (size_t)ceil_div(M < 128 ? M : 128, plan.splits) * plan.width * 4;
+}
+
+// How the adapters' inner products v are computed.
+enum Inner {
+    kNone,   // no adapters
+    kLoads,  // inner_kernel
+    kNamed,  // kInner: the adapters that a tile's tokens name
+    kEvery   // kInnerAll
+};
+
+struct ProjPlan {
+    Plan proj;
+    Inner inner;
+    Plan v;                       // kNamed, kEvery
+    bool direct;                  // v B^T by plain products
+    int per_tile, parts, groups;  // kNamed, as in GemmArgs
+};
+
+ProjPlan plan_proj(int T, int K, int N, int n, int rank, int num_sms, const ClusterFill &fill) {
+    GemmArgs g = {};
+    g.M = T;
+    g.N = N;
+    g.kb = ceil_div(K, 64);
+    ProjPlan p = {};
+    // (the same plan with and without adapters: a token without one gets the
+    // plain projection's bits)
+    p.proj = make_plan(kProj, g, num_sms, fill);
+    if (n == 0) return p;
+    // Inner products by plain loads: x once per four ranks and A once per token
+    // (2.5 T rank K bytes), or per up to four tokens of a run (1 to 2.5),
+    // through L2 at about 6 TB/s, and 2 us for each time the SMs fill with
+    // CTAs; or by kInner, 6.5 us and 0.4 per K block.
+    const int mt = ceil_div(T, 128);
+    int inner_splits = 1;
+    for (int l = 1; l < 4 && fill.ctas[l] >= 1 << l; ++l) {
+        if (2 * mt * inner_splits > num_sms || g.kb / (2 * inner_splits) < 4) break;
+        inner_splits *= 2;
+    }
+    const int64_t ctas = (int64_t)T * rank / 4;
+    const double inner_us = ctas > 8 * num_sms
+                                ? 1.6 * T * (double)rank * K / 6e6 + 2.0 * ceil_div(ctas / 4, 4 * num_sms)
+                                : 2.5 * T * (double)rank * K / 6e6 + 2.0;
+    // v B^T by plain products: about 2.2 us for two groups of four outputs per
+    // thread and 16 ranks, part of it beside the K loop; or by appended
+    // blocks, 1.8 us each for the adapters that a tile may name (the tokens of
+    // a long batch are taken to come in runs).
+    const int rows = T < 128 ? T : 128;
+    const int items = ceil_div(rows, p.proj.splits) * (p.proj.width / 4);
+    const int distinct = T <= 64 ? (n < T ? n : T) : (n < 12 ? n : 12);
+    const int blocks = ceil_div(adapter_blocks(distinct, rank), p.proj.splits);
+    const double direct_us = 2.2 * ceil_div(items, 2 * kGroup) * ceil_div(rank, 16);
+    p.direct = !p.proj.pairs && delta_bytes(T, p.proj) <= kMaxDelta &&
+               direct_us < 0.3 * p.proj.us + 0.5 + 1.8 * blocks;
+    const double list_us = 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
+    if (!p.proj.pairs && inner_us < list_us) {
+        p.inner = kLoads;
+        return p;
+    }
+    // Every adapter's A in one product (however the tokens name them), where
+    // that is not much more than kInner takes for tokens that come in runs;
+    // for tokens that name adapters at random kInner takes a pass over x for
+    // every 128 columns of a tile's adapters.
+    if (n <= 65536 / rank) {
+        GemmArgs ga = g;
+        ga.N = n * rank;
+        p.v = make_plan(kInnerAll, ga, num_sms, fill);
+        if (p.v.us < 1.5 * (p.proj.pairs ? 2.0 * T * K / 3.7e6 + 8 : list_us)) {
+            p.inner = kEvery;
+            return p;
+        }
+    }
+    p.inner = kNamed;
+    const int lines = rank < 128 ? rank : 128;
+    p.per_tile = 128 / lines;
+    p.parts = ceil_div(rank, 128);
+    // SMs that K splits leave go to clusters that share a row tile's
+    // adapters (a split always has work, such a cluster may find none),
+    // fewer adapters at a time if that gives each of them some
+    p.v = {0, false, inner_splits, 128, 128, 1};
+    const int most = n < 128 ? n : 128;
+    p.groups = num_sms / (mt * inner_splits);
+    if (p.groups < 1) p.groups = 1;
+    while (p.per_tile > 1 && ceil_div(most, p.per_tile) < p.groups) p.per_tile = (p.per_tile + 1) / 2;
+    p.v.cols = (p.per_tile * lines + 15) / 16 * 16;
+    const int tiles = p.parts > 1 ? most * p.parts : ceil_div(most, p.per_tile);
+    if (p.groups > tiles) p.groups = tiles;
+    return p;
 }
 
 // `beside`: the launch and one after it are to share the SMs (kInner and the
@@ -1464,17 +1551,15 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
     ClusterFill fill;
     cudaError_t e = cluster_fill(num_sms, &fill);
     if (e != cudaSuccess) return e;
+    const ProjPlan plan = plan_proj(p.T, p.K, p.N, p.n, p.rank, num_sms, fill);
     GemmArgs g = {};
     g.status = p.status;
     g.polls = p.polls;
     g.M = p.T;
     g.N = p.N;
     g.kb = ceil_div(p.K, 64);
-    // (the same plan with and without adapters: a token without one gets the
-    // plain projection's bits)
-    const Plan plan = make_plan(kProj, g, num_sms, fill);
     Maps m;
-    bool beside = false;
+    const bool beside = plan.inner == kNamed && !plan.proj.pairs;
     if (p.n > 0) {
         g.ids = p.ids;
         g.scale = p.scale;
@@ -1482,74 +1567,60 @@ cudaError_t launch_proj_tc(const AdapterParams &p, int num_sms, cudaStream_t s) 
         g.v = reinterpret_cast<uint16_t *>(p.v);
         g.n = p.n;
         g.rank = p.rank;
-        // Inner products by plain loads: x once per four ranks and A once per token
-        // (2.5 T rank K bytes), or per up to four tokens of a run (1 to 2.5),
-        // through L2 at about 6 TB/s, and 2 us for each time the SMs fill with
-        // CTAs; or by kInner, 6.5 us and 0.4 per K block.
-        const int mt = ceil_div(p.T, 128);
-        int inner_splits = 1;
-        while (inner_splits < kMaxSplits && 2 * mt * inner_splits <= num_sms && g.kb / (2 * inner_splits) >= 4)
-            inner_splits *= 2;
-        const int64_t ctas = (int64_t)p.T * p.rank / 4;
-        const double inner_us = ctas > 8 * num_sms
-                                    ? 1.6 * p.T * (double)p.rank * p.K / 6e6 + 2.0 * ceil_div(ctas / 4, 4 * num_sms)
-                                    : 2.5 * p.T * (double)p.rank * p.K / 6e6 + 2.0;
-        // v B^T by plain products: about 2.2 us for two groups of four outputs per
-        // thread and 16 ranks, part of it beside the K loop; or by appended
-        // blocks, 1.8 us each for the adapters that a tile may name (the tokens of
-        // a long batch are taken to come in runs).
-        const int rows = p.T < 128 ? p.T : 128;
-        const int items = ceil_div(rows, plan.splits) * (plan.width / 4);
-        const int distinct = p.T <= 64 ? (p.n < p.T ? p.n : p.T) : (p.n < 12 ? p.n : 12);
-        const int blocks = ceil_div(adapter_blocks(distinct, p.rank), plan.splits);
-        const double direct_us = 2.2 * ceil_div(items, 2 * kGroup) * ceil_div(p.rank, 16);
-        g.direct = !plan.pairs && delta_bytes(p.T, plan) <= kMaxDelta && direct_us < 0.3 * plan.us + 0.5 + 1.8 * blocks;
-        const bool plain = !plan.pairs && inner_us < 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
-        // Every adapter's A in one product (however the tokens name them), where
-        // that is not much more than kInner takes for tokens that come in runs;
-        // for tokens that name adapters at random kInner takes a pass over x for
-        // every 128 columns of a tile's adapters.
-        GemmArgs ga = g;
-        ga.N = p.n <= 65536 / p.rank ? p.n * p.rank : 0;
-        const Plan every = ga.N ? make_plan(kInnerAll, ga, num_sms, fill) : Plan{1e30};
-        const double list_us = plan.pairs ? 2.0 * p.T * p.K / 3.7e6 + 8 : 6.5 + 0.4 * ceil_div(g.kb, inner_splits);
-        const bool all = !plain && every.us < 1.5 * list_us;
-        beside = !plan.pairs && !plain && !all;
-        if (plain) {
+        g.direct = plan.direct;
+        g.per_tile = plan.per_tile;
+        g.parts = plan.parts;
+        g.groups = plan.groups;
+        if (plan.inner == kLoads) {
             if ((e = launch_inner(p, true, num_sms, s)) != cudaSuccess) return e;
-        } else if (all) {
-            if ((e = map_tokens(&m.a, p.x, p.T, p.K, every.pairs)) != cudaSuccess) return e;
-            if ((e = map_weight(&m.b0, p.a, ga.N, p.K, every)) != cudaSuccess) return e;
+        } else if (plan.inner == kEvery) {
+            GemmArgs ga = g;
+            ga.N = p.n * p.rank;
+            if ((e = map_tokens(&m.a, p.x, p.T, p.K, plan.v.pairs)) != cudaSuccess) return e;
+            if ((e = map_weight(&m.b0, p.a, ga.N, p.K, plan.v)) != cudaSuccess) return e;
             m.b1 = m.b0;
-            if ((e = launch_gemm<kInnerAll, 0>(m, ga, every, num_sms, s)) != cudaSuccess) return e;
+            if ((e = launch_gemm<kInnerAll, 0>(m, ga, plan.v, num_sms, s)) != cudaSuccess) return e;
         } else {
-            const int lines = p.rank < 128 ? p.rank : 128;
             if ((e = map_tokens(&m.a, p.x, p.T, p.K, false)) != cudaSuccess) return e;
-            if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, lines)) != cudaSuccess) return e;
+            if ((e = tc::map_stack(&m.b0, p.a, p.n, p.rank, p.K, p.rank < 128 ? p.rank : 128)) != cudaSuccess)
+                return e;
             m.b1 = m.b0;
-            g.per_tile = 128 / lines;
-            g.parts = ceil_div(p.rank, 128);
-            // SMs that K splits leave go to clusters that share a row tile's
-            // adapters (a split always has work, such a cluster may find none),
-            // fewer adapters at a time if that gives each of them some
-            Plan inner = {0, false, inner_splits, 128, 128, 1};
-            const int most = p.n < 128 ? p.n : 128;
-            g.groups = num_sms / (mt * inner.splits);
-            if (g.groups < 1) g.groups = 1;
-            while (g.per_tile > 1 && ceil_div(most, g.per_tile) < g.groups) g.per_tile = (g.per_tile + 1) / 2;
-            inner.cols = (g.per_tile * lines + 15) / 16 * 16;
-            const int tiles = g.parts > 1 ? most * g.parts : ceil_div(most, g.per_tile);
-            if (g.groups > tiles) g.groups = tiles;
-            e = launch_small<kInner, 0>(m, g, inner, num_sms, beside, s);
-            if (e != cudaSuccess) return e;
+            if ((e = launch_small<kInner, 0>(m, g, plan.v, num_sms, beside, s)) != cudaSuccess) return e;
         }
     }
-    if ((e = map_tokens(&m.a, p.x, p.T, p.K, plan.pairs)) != cudaSuccess) return e;
-    if ((e = map_weight(&m.b0, p.w, p.N, p.K, plan)) != cudaSuccess) return e;
+    if ((e = map_tokens(&m.a, p.x, p.T, p.K, plan.proj.pairs)) != cudaSuccess) return e;
+    if ((e = map_weight(&m.b0, p.w, p.N, p.K, plan.proj)) != cudaSuccess) return e;
     m.b1 = m.b0;
     g.residual = p.residual;
     g.out0 = p.y;
-    return launch_gemm<kProj, 0>(m, g, plan, num_sms, s, beside);
+    return launch_gemm<kProj, 0>(m, g, plan.proj, num_sms, s, beside);
+}
+
+cudaError_t adapter_plan(int T, int K, int N, int n, int rank, int num_sms, const int *cluster_ctas,
+                         AdapterPlan *out) {
+    *out = AdapterPlan{};
+    if (gemv_supported(T, K)) {
+        out->splits = 1;
+        out->inner = n > 0 ? kLoads : kNone;
+        out->inner_splits = n > 0;
+        out->direct = n > 0;
+        return cudaSuccess;
+    }
+    ClusterFill fill = {{num_sms, 0, 0, 0}};
+    if (cluster_ctas) {
+        for (int l = 1; l < 4; ++l) fill.ctas[l] = cluster_ctas[l - 1];
+    } else {
+        const cudaError_t e = cluster_fill(num_sms, &fill);
+        if (e != cudaSuccess) return e;
+    }
+    const ProjPlan p = plan_proj(T, K, N, n, rank, num_sms, fill);
+    out->products = p.proj.pairs ? 2 : 1;
+    out->splits = p.proj.splits;
+    out->inner = p.inner;
+    out->inner_splits = p.inner == kNone ? 0 : p.inner == kLoads ? 1 : p.v.splits;
+    out->direct = p.direct;
+    out->groups = p.groups;
+    return cudaSuccess;
 }
 
 }  // namespace moe

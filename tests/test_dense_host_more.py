@@ -1,4 +1,7 @@
 """More host-side checks of the dense feed-forward calls."""
+import math
+import random
+
 import pytest
 
 import packed_mxfp4_w4a16_b200 as moe
@@ -8,3 +11,35 @@ def test_spin_limit_refusal():
     with pytest.raises(moe.MoEError):
         moe.moe_dense_set_spin_limit(-1)
     moe.moe_dense_set_spin_limit(1 << 22)
+
+
+def test_plan_refusals_and_the_smallest_calls():
+    ctas = (148, 144, 128)
+    for bad in (dict(T=0), dict(T=-1), dict(K=12), dict(rank=9), dict(n_adapters=-1), dict(num_sms=-1),
+                dict(cluster_ctas=None), dict(num_sms=0)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_adapter_proj_plan(**{**dict(T=20, K=64, N=32, n_adapters=2, rank=8, num_sms=148,
+                                               cluster_ctas=ctas), **bad})
+    p = moe.moe_adapter_proj_plan(8, 64, 32, num_sms=148, cluster_ctas=ctas)
+    assert p["products"] == "streamed" and p["inner"] == "none" and not p["direct"]
+    p = moe.moe_adapter_proj_plan(9, 64, 32, 2, 8, num_sms=148, cluster_ctas=ctas)
+    assert p["products"] == "single" and p["inner"] == "loads"
+    # few tokens that do not fit in shared memory beside the weights
+    assert moe.moe_adapter_proj_plan(8, 40000, 64, num_sms=148, cluster_ctas=ctas)["products"] == "single"
+
+
+@pytest.mark.parametrize("ctas", [(0, 0, 0), (148, 0, 0), (146, 140, 0), (148, 144, 128)])
+def test_only_clusters_that_fit_are_planned(ctas):
+    most = max([1] + [2 << i for i in range(3) if ctas[i]])
+    rng = random.Random(5)
+    pick = lambda lo, hi, step: max(step, int(math.exp(rng.uniform(math.log(lo), math.log(hi)))) // step * step)
+    seen = set()
+    for _ in range(3000):
+        n, rank = pick(1, 1200, 1), rng.choice([8, 16, 24, 64, 136, 256])
+        p = moe.moe_adapter_proj_plan(pick(1, 9000, 1), pick(8, 9000, 8), pick(8, 9000, 8), n, rank, num_sms=148,
+                                      cluster_ctas=ctas)
+        assert p["splits"] <= most and p["inner_splits"] <= most
+        assert p["products"] != "pairs" or most > 1
+        seen.add((p["products"], p["inner"], p["direct"]))
+    assert {i for _, i, _ in seen} == {"loads", "named", "every"}
+    assert ("single", "every", True) in seen and ("single", "named", False) in seen
