@@ -700,6 +700,8 @@ big_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CU
                 AppendRows f;
                 if (blocks)
                     fetch_block(f, s_ad, g, 0, m + rank * 128, rank * 128, n + rank * half_cols, half_cols, tid, true);
+                else if (t == pair)
+                    pdl_wait();  // the buffer is handed back by a warp that waits for v
 #pragma unroll 1
                 for (int e = 0; e < (blocks ? blocks : 1); ++e, ++x) {
                     if (x > 0) {
