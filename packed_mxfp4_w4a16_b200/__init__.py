@@ -366,6 +366,12 @@ def moe_stack_set_spin_limit(s: int, polls: int) -> None:
 # are written to cost little.
 
 _BF16 = torch.bfloat16
+_MOST = 2 ** 31 - 1  # larger integers would reach the C calls cut to 32 bits
+
+
+def _in_range(name, *values):
+    if max(values) > _MOST or min(values) < -_MOST:
+        raise MoEError(name, -1)
 
 
 def _is(t, dtype, shape):
@@ -425,7 +431,7 @@ def _gated_shapes(x, w_gate, w_up, name):
         (T, H), (I, K) = x.shape, w_gate.shape
         ok = (H == K and w_up.shape == w_gate.shape and x.dtype is _BF16 and w_gate.dtype is _BF16
               and w_up.dtype is _BF16 and x.is_contiguous() and w_gate.is_contiguous()
-              and w_up.is_contiguous())
+              and w_up.is_contiguous() and T <= _MOST and H <= _MOST and I <= _MOST)
     except (AttributeError, ValueError):  # None, or not two dimensions
         ok = False
     if not ok:
@@ -454,6 +460,7 @@ def moe_gated_ffn(x, w_gate, w_up, act=ACT_SILU, h=None, flags=0, x_norm=None, s
 @functools.lru_cache(maxsize=4096)
 def moe_gated_ffn_backward_workspace_bytes(T: int, H: int, I: int) -> int:
     n = C.c_size_t()
+    _in_range("moe_gated_ffn_backward_workspace_bytes", T, H, I)
     check("moe_gated_ffn_backward_workspace_bytes",
           load().moe_gated_ffn_backward_workspace_bytes(T, H, I, C.byref(n)))
     return n.value
@@ -493,6 +500,7 @@ def moe_gated_ffn_backward(x, w_gate, w_up, dh, act=ACT_SILU, dx=None, dw_gate=N
 @functools.lru_cache(maxsize=4096)
 def moe_adapter_proj_workspace_bytes(T: int, K: int, N: int, n_adapters: int, rank: int) -> int:
     n = C.c_size_t()
+    _in_range("moe_adapter_proj_workspace_bytes", T, K, N, n_adapters, rank)
     check("moe_adapter_proj_workspace_bytes",
           load().moe_adapter_proj_workspace_bytes(T, K, N, n_adapters, rank, C.byref(n)))
     return n.value
@@ -509,7 +517,7 @@ def moe_adapter_proj(x, w, lora_a=None, lora_b=None, lora_scale=None, adapter_id
     try:
         (T, K), (N, L) = x.shape, w.shape
         ok = (K == L and x.dtype is _BF16 and w.dtype is _BF16 and x.is_contiguous()
-              and w.is_contiguous())
+              and w.is_contiguous() and T <= _MOST and K <= _MOST and N <= _MOST)
     except (AttributeError, ValueError):
         ok = False
     if not ok:
@@ -552,6 +560,7 @@ def moe_adapter_proj_plan(T, K, N, n_adapters=0, rank=0, num_sms=0, cluster_ctas
     """Which kernels a moe_adapter_proj call of these sizes launches, on the
     current device or on one of ``num_sms`` SMs that runs ``cluster_ctas`` =
     (CTAs at once in clusters of 2, of 4, of 8)."""
+    _in_range("moe_adapter_proj_plan", T, K, N, n_adapters, rank, num_sms, *(cluster_ctas or ()))
     plan = (C.c_int * 6)()
     ctas = None if cluster_ctas is None else (C.c_int * 3)(*cluster_ctas)
     check("moe_adapter_proj_plan", load().moe_adapter_proj_plan(T, K, N, n_adapters, rank, num_sms, ctas, plan))
@@ -570,6 +579,7 @@ def moe_dense_status(stream=None) -> int:
 
 def moe_dense_set_spin_limit(polls: int) -> None:
     """Polls of each bounded wait of later dense calls (default 2^22)."""
+    _in_range("moe_dense_set_spin_limit", polls)
     check("moe_dense_set_spin_limit", load().moe_dense_set_spin_limit(polls))
 
 

@@ -3,6 +3,7 @@ import math
 import random
 
 import pytest
+import torch
 
 import packed_mxfp4_w4a16_b200 as moe
 
@@ -43,3 +44,38 @@ def test_only_clusters_that_fit_are_planned(ctas):
         seen.add((p["products"], p["inner"], p["direct"]))
     assert {i for _, i, _ in seen} == {"loads", "named", "every"}
     assert ("single", "every", True) in seen and ("single", "named", False) in seen
+
+
+class NoCalls:
+    """In the library's place: a call that gets this far fails the test."""
+
+    def __getattr__(self, name):
+        if name == "moe_status_string":
+            return moe._lib.load().moe_status_string
+        raise AssertionError(f"{name} was called")
+
+
+BIG = 2 ** 32 + 8  # 8 in 32 bits
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Integers that do not fit the C calls are refused, not cut to 32 bits."""
+    for call in (lambda v: moe.moe_gated_ffn_backward_workspace_bytes(v, 64, 40),
+                 lambda v: moe.moe_gated_ffn_backward_workspace_bytes(8, v, 40),
+                 lambda v: moe.moe_adapter_proj_workspace_bytes(v, 64, 32, 2, 8),
+                 lambda v: moe.moe_adapter_proj_workspace_bytes(8, 64, 32, v, 8),
+                 lambda v: moe.moe_adapter_proj_plan(v, 64, 32, num_sms=148, cluster_ctas=(148, 144, 128)),
+                 lambda v: moe.moe_dense_set_spin_limit(v)):
+        for v in (BIG, -2 ** 32 + 8):
+            with pytest.raises(moe.MoEError):
+                call(v)
+    # tensors of that many rows, without memory behind them
+    monkeypatch.setattr(moe, "load", NoCalls)
+    t = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device="meta")
+    for call in (lambda: moe.moe_gated_ffn(t(BIG, 8), t(8, 8), t(8, 8)),
+                 lambda: moe.moe_gated_ffn(t(1, 8), t(BIG, 8), t(BIG, 8)),
+                 lambda: moe.moe_gated_ffn_backward(t(BIG, 8), t(8, 8), t(8, 8), t(BIG, 8)),
+                 lambda: moe.moe_adapter_proj(t(BIG, 8), t(8, 8)),
+                 lambda: moe.moe_adapter_proj(t(1, BIG), t(8, BIG))):
+        with pytest.raises(moe.MoEError):
+            call()
