@@ -495,10 +495,12 @@ MOE_API int moe_forward_noalloc_status(void *stream, unsigned *device_status);
  * act(g) are not rounded on the way to h.
  *
  * Shapes: 0 <= T <= 2^30 (T = 0 is accepted: forward calls enqueue nothing,
- * the backward call zeroes the weight gradients); every other dimension a
- * multiple of 8 in [8, 65536].  Up to 8 tokens stream the weights through
- * mma.sync products (decode), more run on tcgen05 tiles; results of the same
- * row may differ in the last bits between batch sizes.
+ * the backward call sets the weight gradients to zero by memset); every other
+ * dimension a multiple of 8 in [8, 65536].  Up to 8 tokens stream the weights
+ * through mma.sync products (decode) while the tokens fit in shared memory
+ * beside them (8 of 11000 elements do, 1 of 65536), more run on tcgen05 tiles;
+ * results of the same row may differ in the last bits between batch sizes and,
+ * with adapters, between batches that name other adapters.
  *
  * Device problems (a bounded wait that gave up, a bad adapter id) are OR-ed
  * into one status word per GPU, read by moe_dense_status. */
@@ -563,9 +565,9 @@ MOE_API int moe_adapter_proj_workspace_bytes(int T, int K, int N, int n_adapters
  * name adapters in any order; tokens of one request next to each other are
  * fastest.  An adapter with infinities or NaN reaches only the tokens that
  * name it.  The inner product scale * (A x) is rounded to BF16 once, as the
- * operand of the product with B, where T > 8 (FP32 for fewer).  Workspace: device, 256-byte
- * aligned; nothing in it is kept between calls; calls that may run at the
- * same time need workspaces of their own.  y must not overlap x, w, the
+ * operand of the product with B (FP32 where the weights are streamed).
+ * Workspace: device, 256-byte aligned; nothing in it is kept between calls;
+ * calls that may run at the same time need workspaces of their own.  y must not overlap x, w, the
  * adapters or the workspace.  Errors: ARG, NOT_DEVICE, ALIGN, WORKSPACE,
  * UNSUPPORTED, CUDA. */
 MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint16_t *w,

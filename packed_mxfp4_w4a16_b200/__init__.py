@@ -571,7 +571,8 @@ def moe_adapter_proj_plan(T, K, N, n_adapters=0, rank=0, num_sms=0, cluster_ctas
 
 def moe_dense_status(stream=None) -> int:
     """Status bits of the dense calls on the current device since the last
-    read (synchronises `stream`), cleared."""
+    read (synchronises `stream`), cleared. The word is one for all streams and
+    layers of the GPU: whoever reads first gets the bits."""
     v = C.c_uint()
     check("moe_dense_status", load().moe_dense_status(_s(stream), C.byref(v)))
     return v.value
@@ -703,7 +704,8 @@ class DenseFFN:
     def forward(self, x, adapter_ids=None, residual=None, y=None, rmsnorm=False, stream=None):
         """y [T, H] for x [T, H], T <= max_tokens.  rmsnorm: x is a residual
         stream, the layer runs on its RMSNorm.  adapter_ids int32 [T] (-1:
-        none); None: no adapters.  residual may be y."""
+        none); None: no adapters.  A layer without adapters does not look at
+        them.  residual may be y."""
         T = x.shape[0]
         if T > self.max_tokens:
             raise MoEError("DenseFFN.forward", -5)

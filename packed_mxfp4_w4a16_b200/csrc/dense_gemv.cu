@@ -3,7 +3,8 @@
 //
 //   gated  h[t][i] = act(Wg[i] x[t]) * (Wu[i] x[t])
 //   proj   y[t][n] = W[n] x[t] + sum_j v[t][j] B[id_t][n][j] (+ residual)
-//   inner  v[t][j] = scale * (A[id_t][j] x[t])          (FP32, workspace)
+//   inner  v[t][j] = scale * (A[id_t][j] x[t])          (workspace; FP32, or BF16 for
+//          the tensor-core projection of more tokens)
 //
 // One CTA per SM owns a contiguous range of output rows (ranges differ by at
 // most one row, so every SM streams the same bytes) and walks it in tiles of
