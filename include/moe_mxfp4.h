@@ -587,8 +587,8 @@ MOE_API int moe_adapter_proj(const uint16_t *x, int T, int K, int N, const uint1
  *   [4] products with B: 1 plain, 0 as columns appended to K (or none)
  *   [5] with [2] = 2: clusters that share a row tile's adapters, else 0
  * num_sms 0 and cluster_ctas NULL: on the current device.  Otherwise on a GPU
- * of num_sms SMs that runs cluster_ctas[0 .. 2] CTAs at once in clusters of 2, 4
- * and 8 (a host without a GPU will do).  Errors: ARG, UNSUPPORTED, CUDA. */
+ * of num_sms SMs that runs cluster_ctas[0 .. 2] CTAs, one per SM, at once in
+ * clusters of 2, 4 and 8 (a host without a GPU will do).  Errors: ARG, UNSUPPORTED, CUDA. */
 MOE_API int moe_adapter_proj_plan(int T, int K, int N, int n_adapters, int rank, int num_sms,
                                   const int *cluster_ctas, int *plan);
 

@@ -253,6 +253,8 @@ int moe_adapter_proj_plan(int T, int K, int N, int n_adapters, int rank, int num
     int rc = moe_adapter_proj_workspace_bytes(T, K, N, n_adapters, rank, &need);
     if (rc != MOE_OK) return rc;
     if (!plan || T == 0 || num_sms < 0 || (num_sms > 0) != (cluster_ctas != nullptr)) return MOE_ERR_ARG;
+    for (int l = 0; cluster_ctas && l < 3; ++l)  // one CTA per SM
+        if (cluster_ctas[l] < 0 || cluster_ctas[l] > num_sms) return MOE_ERR_ARG;
     if (num_sms == 0) {
         int dev = 0;
         DeviceInfo d;

@@ -79,3 +79,15 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
                  lambda: moe.moe_adapter_proj(t(1, BIG), t(8, BIG))):
         with pytest.raises(moe.MoEError):
             call()
+
+
+def test_plan_for_the_smallest_devices():
+    """More CTAs than SMs are refused; a single SM has no pairs."""
+    for ctas in ((2, 0, 0), (0, 0, 8), (-1, 0, 0)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_adapter_proj_plan(300, 64, 32, 2, 8, num_sms=1, cluster_ctas=ctas)
+    for sms, ctas in ((1, (0, 0, 0)), (1, (1, 1, 1)), (2, (2, 0, 0)), (7, (6, 4, 0))):
+        for T in (1, 20, 129, 5000, 2 ** 30):
+            for n, rank in ((0, 0), (1, 8), (300, 256), (2 ** 31 - 1, 8)):
+                p = moe.moe_adapter_proj_plan(T, 65536, 8, n, rank, num_sms=sms, cluster_ctas=ctas)
+                assert sms > 1 or (p["products"] != "pairs" and p["splits"] == 1)
