@@ -87,3 +87,36 @@ def test_outputs_outlive_their_readers_on_the_current_stream():
         again = moe.moe_gated_ffn(nx, wg, wu, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(copy, want) and torch.equal(again, other)
+
+
+@pytest.mark.parametrize("T", [3, 300])
+def test_a_captured_branch_on_another_stream(T):
+    """Calls on a second stream that takes part in a capture: a graph of two
+    branches whose outputs and workspaces come from the graph's memory."""
+    x, wg, wu = normal((T, 264), 1, 1), normal((328, 264), 0.06, 2), normal((328, 264), 0.06, 3)
+    dh, wd = normal((T, 328), 0.1, 4), normal((264, 328), 0.05, 5)
+    a, b, sc = normal((5, 24, 328), 0.05, 6), normal((5, 264, 24), 0.05, 7), torch.ones(5, device="cuda")
+    ids = torch.arange(T, device="cuda", dtype=torch.int32) % 6 - 1
+
+    def branch(stream):
+        h = moe.moe_gated_ffn(x, wg, wu, stream=stream)
+        return [h, moe.moe_adapter_proj(h, wd, a, b, sc, ids, stream=stream),
+                *moe.moe_gated_ffn_backward(x, wg, wu, dh, stream=stream)]
+
+    want = branch(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        first = branch(side)
+        second = branch(None)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for t in first + second:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for out in (first, second):
+            assert all(torch.equal(p, q) for p, q in zip(out, want))
+    assert moe.moe_dense_status() == 0
