@@ -682,7 +682,8 @@ class DenseFFN:
 
     The layer keeps the buffers of up to ``max_tokens`` tokens (h, the
     normalised input, the adapters' workspace), so its calls must be ordered
-    on the GPU; captured in a CUDA graph they stay valid as long as the layer."""
+    on the GPU; captured in a CUDA graph they stay valid as long as the layer.
+    Making a layer waits for the current stream."""
 
     def __init__(self, w_gate, w_up, w_down, act=ACT_SILU, lora=None, max_tokens=4):
         moe_device_check()
@@ -700,6 +701,10 @@ class DenseFFN:
             need = max(moe_adapter_proj_workspace_bytes(t, self.I, self.H, n, rank)
                        for t in {max_tokens, min(max_tokens, 8)})
         self.workspace = w_gate.new_empty(need, dtype=torch.uint8)
+        # the buffers may be used on any stream, so the current one must be done
+        # with what it had in their place (nothing may be asked of it in a capture)
+        if w_gate.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(w_gate.device).synchronize()
 
     def forward(self, x, adapter_ids=None, residual=None, y=None, rmsnorm=False, stream=None):
         """y [T, H] for x [T, H], T <= max_tokens.  rmsnorm: x is a residual

@@ -120,3 +120,20 @@ def test_a_captured_branch_on_another_stream(T):
         for out in (first, second):
             assert all(torch.equal(p, q) for p, q in zip(out, want))
     assert moe.moe_dense_status() == 0
+
+
+@pytest.mark.parametrize("T", [4, 600])
+def test_buffers_of_a_layer_wait_for_no_work_of_the_current_stream(T):
+    """The buffers that a layer allocates when it is made, used on another stream."""
+    H, I, rank = 1024, 1536, 16
+    x, wg, wu, wd = normal((T, H), 1, 1), normal((I, H), 0.03, 2), normal((I, H), 0.03, 3), normal((H, I), 0.03, 5)
+    lora = (normal((3, rank, I), 0.03, 6), normal((3, H, rank), 0.1, 7), torch.ones(3, device="cuda"))
+    ids = torch.arange(T, device="cuda", dtype=torch.int32) % 3
+    want = moe.DenseFFN(wg, wu, wd, lora=lora, max_tokens=T).forward(x, ids, rmsnorm=True)
+    side = torch.cuda.Stream()
+    words = moe.moe_adapter_proj_workspace_bytes(T, I, H, 3, rank) // 2
+    pending = PendingWork([T * I, T * H, words])
+    layer = moe.DenseFFN(wg, wu, wd, lora=lora, max_tokens=T)
+    y = layer.forward(x, ids, rmsnorm=True, stream=side)
+    pending.check()
+    assert torch.equal(y, want)
