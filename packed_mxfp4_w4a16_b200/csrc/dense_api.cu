@@ -277,12 +277,13 @@ int moe_dense_status(void *stream, unsigned *device_status) {
     if (rc != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     unsigned v = 0;
-    static std::mutex reading;  // one reader at a time has the taken word
-    std::lock_guard<std::mutex> lock(reading);
     if (cudaStreamSynchronize(s) != cudaSuccess) {
         cudaGetLastError();
         return MOE_ERR_CUDA;
     }
+    // one reader at a time has the taken word, for as long as the read itself takes
+    static std::mutex reading;
+    std::lock_guard<std::mutex> lock(reading);
     take_status_kernel<<<1, 1, 0, s>>>(d.status);
     if (cudaGetLastError() != cudaSuccess ||
         cudaMemcpyAsync(&v, d.status + kTaken, sizeof v, cudaMemcpyDeviceToHost, s) != cudaSuccess ||

@@ -58,3 +58,28 @@ def test_readers_in_several_threads_take_each_bit_once():
         for t in threads:
             t.join()
         assert sorted(seen) == [0, 0, 0, moe.DEVICE_BAD_ADAPTER_ID]
+
+
+def test_a_reader_waits_for_its_own_stream_only():
+    """While one thread waits for a busy stream, another reads on an idle one."""
+    import threading
+
+    moe.moe_dense_status()
+    busy, idle = torch.cuda.Stream(), torch.cuda.Stream()
+    moe.moe_dense_status(idle)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(4_000_000_000)  # about two seconds
+    entered = threading.Event()
+
+    def read():
+        entered.set()
+        moe.moe_dense_status(busy)
+
+    t = threading.Thread(target=read)
+    t.start()
+    entered.wait()
+    threading.Event().wait(0.2)  # well into the other's wait
+    moe.moe_dense_status(idle)
+    assert t.is_alive()
+    t.join()
